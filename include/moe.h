@@ -453,6 +453,62 @@ int moe_balance_loss(const int32_t* idx, const float* gate, int T, int E, int k,
                      void* stream);
 
 /*
+ * The block around the routed experts: y = x + dropout(MoE(n) + FFN(n)) with
+ * n = layer_norm(x).  The pages state the MoE layer alone ([Beam] sec. 2.2
+ * places it in a transformer block); these operators follow their formulas.
+ *
+ * moe_layernorm_fwd -- per row of x: mean and rstd = 1 / sqrt(var + eps)
+ *   (var: mean squared deviation) in fp32, y = (x - mean) rstd weight + bias.
+ *   x: T rows of d (dtype), row r at x + r * ldx elements (ldx >= d); weight,
+ *   bias [d] (wdtype: MOE_F32 or MOE_BF16, independent of dtype) or NULL
+ *   (ones, zeros).  y [T,d] (dtype) out, contiguous; it may be x itself when
+ *   ldx == d.  mean, rstd [T] fp32 out (both, or both NULL).  Any d >= 1 and
+ *   any element alignment; rows of 16-byte multiples at 16-byte aligned
+ *   addresses are fastest.
+ * moe_layernorm_bwd -- from dy and what the forward returned, with g = dy
+ *   weight and xh = (x - mean) rstd:
+ *   dx = rstd (g - mean_c(g) - xh mean_c(g xh)) + addend;
+ *   dweight = sum_t dy xh, dbias = sum_t dy.
+ *   dy, x, addend: T rows of d (dtype) with row strides lddy, ldx, ldadd;
+ *   addend or NULL: the gradient of the branch around the norm, joined in
+ *   the same pass.  dx [T,d] (dtype) out, contiguous; it must not overlap
+ *   the inputs.  dweight, dbias [d] fp32 out, either may be NULL; zeros when
+ *   T = 0.  Sums run in a fixed order (deterministic).  ws: at least
+ *   moe_layernorm_bwd_workspace_size() bytes, 16-byte aligned (not needed
+ *   without dweight and dbias).
+ */
+int moe_layernorm_fwd(const void* x, int64_t ldx, const void* weight, const void* bias, int T,
+                      int d, int dtype, int wdtype, float eps, void* y, float* mean, float* rstd,
+                      void* stream);
+size_t moe_layernorm_bwd_workspace_size(int T, int d);
+int moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                      const float* mean, const float* rstd, const void* addend, int64_t ldadd,
+                      int T, int d, int dtype, int wdtype, void* dx, float* dweight, float* dbias,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_dropout_fwd -- out[i] = residual[i] + (keep_i ? x[i] / (1 - q) : 0) over
+ *   n contiguous elements (dtype), one rounding; residual or NULL (zeros).
+ *   q = thr / 65536 with thr = round(65536 p) (halves to even): p in [0, 1]
+ *   counts in steps of 2^-16.  keep_i: element i takes 16 bits of
+ *   Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2,
+ *   3", 2011) with key = seed and counter words (i / 8 low, i / 8 high,
+ *   offset low, offset high): half i % 2 (0: low) of word (i % 8) / 2; it is
+ *   kept where they are >= thr.  A dropped element adds nothing, also when
+ *   it is infinite or NaN.
+ *   rng [2] int64 (device): seed, offset.  They are read on the device, so a
+ *   captured graph draws a new mask when the caller changes them between
+ *   replays (one offset per call and step).  out may be x or residual.
+ * moe_dropout_bwd -- dx[i] = keep_i ? dout[i] / (1 - q) : 0 with the mask
+ *   drawn again from the same rng and p; the residual's gradient is dout.
+ *   dx may be dout.
+ */
+int moe_dropout_fwd(const void* x, const void* residual, int64_t n, double p, const int64_t* rng,
+                    int dtype, void* out, void* stream);
+int moe_dropout_bwd(const void* dout, int64_t n, double p, const int64_t* rng, int dtype, void* dx,
+                    void* stream);
+
+/*
  * moe_check_status -- synchronises `stream`, then reads and clears the
  * device status word of the current device.  Returns MOE_OK, MOE_ERR_CUDA
  * (a CUDA error), MOE_ERR_DEVICE_TIMEOUT if a bounded device wait expired

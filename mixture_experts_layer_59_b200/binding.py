@@ -35,7 +35,8 @@ EXPORTS = [
     "moe_debug_expire_next_wait", "moe_gather_rows", "moe_ep_dispatch_counts",
     "moe_ep_receive_plan", "moe_expert_rows_fwd_workspace_size", "moe_expert_rows_fwd",
     "moe_expert_rows_bwd_workspace_size", "moe_expert_rows_bwd", "moe_token_bwd_workspace_size",
-    "moe_token_bwd",
+    "moe_token_bwd", "moe_layernorm_fwd", "moe_layernorm_bwd_workspace_size", "moe_layernorm_bwd",
+    "moe_dropout_fwd", "moe_dropout_bwd",
 ]
 
 _lib = None
@@ -48,6 +49,7 @@ class MoEError(RuntimeError):
 
 
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_i64, _f, _d = ctypes.c_int64, ctypes.c_float, ctypes.c_double
 
 _SIGS = {
     "moe_version": (_i, []),
@@ -86,6 +88,12 @@ _SIGS = {
     "moe_expert_rows_bwd": (_i, [_vp] * 8 + [_i] * 5 + [_vp] * 6 + [_sz, _vp]),
     "moe_token_bwd_workspace_size": (_sz, [_i] * 5),
     "moe_token_bwd": (_i, [_vp] * 8 + [_i] + [_vp] * 3 + [_i] * 6 + [_vp] * 4 + [_sz, _vp]),
+    "moe_layernorm_fwd": (_i, [_vp, _i64, _vp, _vp] + [_i] * 4 + [_f] + [_vp] * 4),
+    "moe_layernorm_bwd_workspace_size": (_sz, [_i, _i]),
+    "moe_layernorm_bwd": (_i, [_vp, _i64, _vp, _i64] + [_vp] * 4 + [_i64] + [_i] * 4 + [_vp] * 4
+                          + [_sz, _vp]),
+    "moe_dropout_fwd": (_i, [_vp, _vp, _i64, _d, _vp, _i, _vp, _vp]),
+    "moe_dropout_bwd": (_i, [_vp, _i64, _d, _vp, _i, _vp, _vp]),
 }
 
 
@@ -504,3 +512,173 @@ def moe_token_bwd(dX_rows, dS, x, w_gate, idx, gate, plan, router_grad=True, gat
                                1 if router_grad else 0, _p(o["dx"]), _p(o["dw_gate"]),
                                _p(o["dlogits"]), _p(ws), ws.numel(), _stream(stream)))
     return o
+
+
+# ------------------------------------------------------------------ the block around the experts
+_CODES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+def _bad(msg, code=MOE_ERR_INVALID_ARG):
+    raise MoEError(code, msg)
+
+
+def _code(name, t):
+    c = _CODES.get(t.dtype)
+    return c if c is not None else _bad(f"{name}: unsupported dtype {t.dtype}", MOE_ERR_UNSUPPORTED)
+
+
+def _check_arg(name, t, shape, dtype, device, rows=False):
+    """t has this shape, dtype and device and is contiguous (rows: or a matrix
+    of contiguous rows at a row stride)."""
+    if t.shape != shape:
+        _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        _bad(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        _bad(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous() and not (rows and t.numel() and (t.stride(1) == 1 or t.shape[1] == 1)
+                                      and t.stride(0) >= t.shape[1]):
+        _bad(f"{name}: must be contiguous" + (" along its rows" if rows else ""))
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class _On:
+    """Runs a call on its tensors' device and the given stream: allocations
+    made inside belong to that stream, so their memory is not handed out
+    again while the stream still uses it."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            _bad(f"tensors must be on a CUDA device, got {device}")
+        self.dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.dev is not None:
+            self.dev.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        if self.dev is not None:
+            self.dev.__exit__(*exc)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None,
+                      stream=None):
+    """Layer norm over the rows of x [T, d]: returns (y [T, d], mean [T] f32,
+    rstd [T] f32).  x may have a row stride; weight and bias [d] are bf16 or
+    fp32 (one dtype for both), or None."""
+    if x.dim() != 2:
+        _bad(f"x: expected a matrix, got {x.dim()} dimensions")
+    T, d = x.shape
+    dev, dt = x.device, _code("x", x)
+    _check_arg("x", x, (T, d), x.dtype, dev, rows=True)
+    wt = weight if weight is not None else bias
+    wdt = MOE_F32 if wt is None else _code("weight", wt)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check_arg(name, t, (d,), wt.dtype, dev)
+    if (mean is None) != (rstd is None):
+        _bad("mean and rstd: pass both or neither")
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty(T, d, device=dev, dtype=x.dtype)
+        else:
+            _check_arg("y", y, (T, d), x.dtype, dev)
+        if mean is None:
+            mean, rstd = torch.empty(2, T, device=dev, dtype=torch.float32).unbind(0)
+        else:
+            _check_arg("mean", mean, (T,), torch.float32, dev)
+            _check_arg("rstd", rstd, (T,), torch.float32, dev)
+        _check(lib().moe_layernorm_fwd(x.data_ptr(), _row_stride(x), _ptr(weight), _ptr(bias), T, d,
+                                       dt, wdt, eps, y.data_ptr(), mean.data_ptr(),
+                                       rstd.data_ptr(), s))
+    return y, mean, rstd
+
+
+def moe_layernorm_bwd_workspace_size(T, d) -> int:
+    return lib().moe_layernorm_bwd_workspace_size(T, d)
+
+
+def moe_layernorm_bwd(dy, x, weight, mean, rstd, addend=None, out=None, ws=None, stream=None):
+    """Backward of moe_layernorm_fwd.  Returns dict dx [T, d] (+ addend),
+    dweight, dbias [d] f32.  dy, x and addend may have row strides."""
+    if x.dim() != 2:
+        _bad(f"x: expected a matrix, got {x.dim()} dimensions")
+    T, d = x.shape
+    dev, dt = x.device, _code("x", x)
+    _check_arg("x", x, (T, d), x.dtype, dev, rows=True)
+    _check_arg("dy", dy, (T, d), x.dtype, dev, rows=True)
+    _check_arg("mean", mean, (T,), torch.float32, dev)
+    _check_arg("rstd", rstd, (T,), torch.float32, dev)
+    if addend is not None:
+        _check_arg("addend", addend, (T, d), x.dtype, dev, rows=True)
+    wdt = MOE_F32 if weight is None else _code("weight", weight)
+    if weight is not None:
+        _check_arg("weight", weight, (d,), weight.dtype, dev)
+    o = dict(out) if out else {}
+    with _On(dev, stream) as s:
+        for name, shape, dtype in (("dx", (T, d), x.dtype), ("dweight", (d,), torch.float32),
+                                   ("dbias", (d,), torch.float32)):
+            if name not in o:
+                o[name] = torch.empty(shape, device=dev, dtype=dtype)
+            else:
+                _check_arg(name, o[name], shape, dtype, dev)
+        if ws is None:
+            ws = torch.empty(max(moe_layernorm_bwd_workspace_size(T, d), 1), device=dev,
+                             dtype=torch.uint8)
+        _check(lib().moe_layernorm_bwd(
+            dy.data_ptr(), _row_stride(dy), x.data_ptr(), _row_stride(x), _ptr(weight),
+            mean.data_ptr(), rstd.data_ptr(), _ptr(addend),
+            0 if addend is None else _row_stride(addend), T, d, dt, wdt, o["dx"].data_ptr(),
+            o["dweight"].data_ptr(), o["dbias"].data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return o
+
+
+def _check_dropout(x, rng):
+    dt = _code("x", x)
+    if not x.is_contiguous():
+        _bad("x: must be contiguous")
+    _check_arg("rng", rng, (2,), torch.int64, x.device)
+    return dt
+
+
+def moe_dropout_fwd(x, p, rng, residual=None, out=None, stream=None):
+    """residual + dropout(x) (residual None: dropout(x)); x of any shape.
+    rng: int64 [2] on the device, (seed, offset); the mask is a function of
+    (seed, offset, element index) alone and is not stored."""
+    dt = _check_dropout(x, rng)
+    if residual is not None:
+        _check_arg("residual", residual, x.shape, x.dtype, x.device)
+    with _On(x.device, stream) as s:
+        if out is None:
+            out = torch.empty_like(x)
+        else:
+            _check_arg("out", out, x.shape, x.dtype, x.device)
+        _check(lib().moe_dropout_fwd(x.data_ptr(), _ptr(residual), x.numel(), p, rng.data_ptr(), dt,
+                                     out.data_ptr(), s))
+    return out
+
+
+def moe_dropout_bwd(dout, p, rng, dx=None, stream=None):
+    """Gradient of moe_dropout_fwd for its x (the residual's is dout itself)."""
+    dt = _check_dropout(dout, rng)
+    with _On(dout.device, stream) as s:
+        if dx is None:
+            dx = torch.empty_like(dout)
+        else:
+            _check_arg("dx", dx, dout.shape, dout.dtype, dout.device)
+        _check(lib().moe_dropout_bwd(dout.data_ptr(), dout.numel(), p, rng.data_ptr(), dt,
+                                     dx.data_ptr(), s))
+    return dx

@@ -1,6 +1,7 @@
 // extern "C" entry points: argument checks, workspace layout, kernel order.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <map>
@@ -817,6 +818,110 @@ int moe_balance_loss(const int32_t* idx, const float* gate, int T, int E, int k,
     return fail(MOE_ERR_WORKSPACE, "balance workspace smaller than moe_balance_loss_workspace_size()");
   return launch_balance_loss(idx, gate, T, E, k, lambda, stats, importance, dgate, ws, ws_bytes,
                              (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------------ layer norm and dropout
+static int check_types(int dtype, int wdtype) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16");
+  if (wdtype != MOE_F32 && wdtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "wdtype must be MOE_F32 or MOE_BF16");
+  return MOE_OK;
+}
+
+static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+#define REQUIRE_ELEM_ALIGNED(p, n)                                                        \
+  do {                                                                                    \
+    if (!aligned_to(p, n))                                                                \
+      return fail(MOE_ERR_INVALID_ARG, #p " must be aligned to its elements");            \
+  } while (0)
+
+int moe_layernorm_fwd(const void* x, int64_t ldx, const void* weight, const void* bias, int T,
+                      int d, int dtype, int wdtype, float eps, void* y, float* mean, float* rstd,
+                      void* stream) {
+  if (int rc = check_types(dtype, wdtype)) return rc;
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0");
+  if (d <= 0) return fail(MOE_ERR_INVALID_ARG, "d must be > 0");
+  if (!(eps >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+  if ((mean == nullptr) != (rstd == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "mean and rstd must be both set or both NULL");
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(y);
+  if (ldx < d) return fail(MOE_ERR_INVALID_ARG, "ldx must be >= d");
+  REQUIRE_ELEM_ALIGNED(x, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(y, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(weight, esize(wdtype));
+  REQUIRE_ELEM_ALIGNED(bias, esize(wdtype));
+  return launch_layernorm_fwd(x, ldx, weight, bias, T, d, dtype, wdtype, eps, y, mean, rstd,
+                              (cudaStream_t)stream);
+}
+
+size_t moe_layernorm_bwd_workspace_size(int T, int d) { return layernorm_bwd_ws_bytes(T, d); }
+
+int moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                      const float* mean, const float* rstd, const void* addend, int64_t ldadd,
+                      int T, int d, int dtype, int wdtype, void* dx, float* dweight, float* dbias,
+                      void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_types(dtype, wdtype)) return rc;
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0");
+  if (d <= 0) return fail(MOE_ERR_INVALID_ARG, "d must be > 0");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (T == 0) {   // no rows: the sums over them are zero
+    for (float* g : {dweight, dbias})
+      if (g != nullptr)
+        if (cudaError_t e = cudaMemsetAsync(g, 0, sizeof(float) * (size_t)d, s))
+          return cuda_fail(e, "layernorm_bwd zero gradients");
+    return MOE_OK;
+  }
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(mean);
+  REQUIRE_PTR(rstd);
+  REQUIRE_PTR(dx);
+  if (lddy < d || ldx < d || (addend != nullptr && ldadd < d))
+    return fail(MOE_ERR_INVALID_ARG, "row strides must be >= d");
+  REQUIRE_ELEM_ALIGNED(dy, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(x, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(addend, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(dx, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(weight, esize(wdtype));
+  if (dweight != nullptr || dbias != nullptr) {
+    if (ws == nullptr || ws_bytes < layernorm_bwd_ws_bytes(T, d))
+      return fail(MOE_ERR_WORKSPACE, "layernorm workspace smaller than moe_layernorm_bwd_workspace_size()");
+    REQUIRE_ALIGNED(ws);
+  }
+  return launch_layernorm_bwd(dy, lddy, x, ldx, weight, mean, rstd, addend, ldadd, T, d, dtype,
+                              wdtype, dx, dweight, dbias, (float*)ws, s);
+}
+
+static int dropout_checked(const void* x, const void* residual, int64_t n, double p,
+                           const int64_t* rng, int dtype, void* out, const char* name,
+                           void* stream) {
+  if (int rc = check_types(dtype, MOE_F32)) return rc;
+  if (n < 0) return fail(MOE_ERR_INVALID_ARG, "n must be >= 0");
+  if (!(p >= 0.0 && p <= 1.0)) return fail(MOE_ERR_INVALID_ARG, "p must be in [0, 1]");
+  if (n == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(rng);
+  REQUIRE_PTR(out);
+  REQUIRE_ELEM_ALIGNED(x, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(residual, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(out, esize(dtype));
+  REQUIRE_ELEM_ALIGNED(rng, sizeof(int64_t));
+  return launch_dropout(x, residual, n, (uint32_t)std::nearbyint(p * 65536.0), rng, dtype, out,
+                        name, (cudaStream_t)stream);
+}
+
+int moe_dropout_fwd(const void* x, const void* residual, int64_t n, double p, const int64_t* rng,
+                    int dtype, void* out, void* stream) {
+  return dropout_checked(x, residual, n, p, rng, dtype, out, "dropout_fwd", stream);
+}
+
+int moe_dropout_bwd(const void* dout, int64_t n, double p, const int64_t* rng, int dtype, void* dx,
+                    void* stream) {
+  return dropout_checked(dout, nullptr, n, p, rng, dtype, dx, "dropout_bwd", stream);
 }
 
 int moe_check_status(void* stream) {

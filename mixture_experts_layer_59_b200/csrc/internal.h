@@ -126,6 +126,21 @@ int launch_ds_rows(const float* ds_part, int nparts, const int32_t* offsets, int
 // the next tensor-core GEMM launch, or 0; taking it clears the request.
 long long take_debug_expire();
 
+// ---------------------------------------------------------------- layer norm (norm.cu)
+int launch_layernorm_fwd(const void* x, int64_t ldx, const void* w, const void* b, int T, int d,
+                         int dtype, int wdtype, float eps, void* y, float* mean, float* rstd,
+                         cudaStream_t s);
+size_t layernorm_bwd_ws_bytes(int T, int d);
+int launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                         const float* mean, const float* rstd, const void* add, int64_t ldadd,
+                         int T, int d, int dtype, int wdtype, void* dx, float* dweight,
+                         float* dbias, float* part, cudaStream_t s);
+
+// ---------------------------------------------------------------- dropout (dropout.cu)
+// out = (residual or 0) + keep * x * 65536 / (65536 - thr); residual may be null.
+int launch_dropout(const void* x, const void* residual, int64_t n, uint32_t thr, const int64_t* rng,
+                   int dtype, void* out, const char* name, cudaStream_t s);
+
 // ---------------------------------------------------------------- MXFP8 (mx.cu, tc_gemm.cu)
 int launch_mx_quant_weights(const void* w1, const void* w3, const void* w2, int E, int d, int f,
                             uint8_t* w13q, uint8_t* w13s, uint8_t* w2q, uint8_t* w2s,

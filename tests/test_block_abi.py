@@ -1,0 +1,74 @@
+"""Host-side checks of the operators around the experts: bad arguments are
+refused before anything is launched (no GPU needed)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from mixture_experts_layer_59_b200 import binding as B
+
+F = ctypes.c_void_p(256)
+ODD = ctypes.c_void_p(257)
+
+
+def ln_fwd(**kw):
+    a = dict(x=F, ldx=256, w=F, b=F, T=4, d=256, dt=B.MOE_BF16, wdt=B.MOE_F32, eps=1e-5, y=F, mean=F, rstd=F)
+    a.update(kw)
+    return B.lib().moe_layernorm_fwd(*a.values(), None)
+
+
+def ln_bwd(**kw):
+    a = dict(dy=F, lddy=256, x=F, ldx=256, w=F, mean=F, rstd=F, add=None, ldadd=0, T=4, d=256, dt=B.MOE_BF16,
+             wdt=B.MOE_F32, dx=F, dw=F, db=F, ws=F, wsb=1 << 30)
+    a.update(kw)
+    return B.lib().moe_layernorm_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=5), -2), (dict(wdt=-1), -2), (dict(T=-1), -1), (dict(d=0), -1), (dict(eps=-1.0), -1),
+    (dict(eps=math.nan), -1), (dict(mean=None), -1), (dict(x=None), -1), (dict(y=None), -1),
+    (dict(ldx=255), -1), (dict(x=ODD), -1), (dict(w=ODD), -1), (dict(T=0, x=None, y=None), 0),
+])
+def test_layernorm_fwd_refusals(kw, code):
+    assert ln_fwd(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=5), -2), (dict(wdt=9), -2), (dict(T=-1), -1), (dict(d=-3), -1), (dict(dy=None), -1),
+    (dict(mean=None), -1), (dict(rstd=None), -1), (dict(dx=None), -1), (dict(lddy=255), -1),
+    (dict(add=F, ldadd=10), -1), (dict(ws=None), -5), (dict(wsb=16), -5), (dict(dx=ODD), -1),
+])
+def test_layernorm_bwd_refusals(kw, code):
+    assert ln_bwd(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), -1), (dict(p=-0.01), -1), (dict(p=1.01), -1), (dict(p=math.nan), -1), (dict(dt=3), -2),
+    (dict(x=None), -1), (dict(rng=None), -1), (dict(out=None), -1), (dict(x=ODD), -1),
+    (dict(rng=ctypes.c_void_p(260)), -1), (dict(n=0, x=None, out=None), 0),
+])
+def test_dropout_refusals(kw, code):
+    a = dict(x=F, res=None, n=100, p=0.1, rng=F, dt=B.MOE_BF16, out=F)
+    a.update(kw)
+    assert B.lib().moe_dropout_fwd(*a.values(), None) == code
+    del a["res"]
+    assert B.lib().moe_dropout_bwd(*a.values(), None) == code
+
+
+def test_binding_refuses_what_it_cannot_launch():
+    x, w = torch.zeros(4, 8), torch.zeros(8)
+    rng = torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: B.moe_layernorm_fwd(x, w),                       # not on a CUDA device
+                 lambda: B.moe_layernorm_fwd(x[0], w),                    # not a matrix
+                 lambda: B.moe_layernorm_fwd(x, w[:5]),                   # wrong width
+                 lambda: B.moe_layernorm_fwd(x.t(), torch.zeros(4)),      # columns contiguous
+                 lambda: B.moe_layernorm_fwd(x.half(), w),                # type
+                 lambda: B.moe_layernorm_fwd(x, w, w.bfloat16()),         # two parameter types
+                 lambda: B.moe_layernorm_bwd(x, x.bfloat16(), w, x[:, 0], x[:, 0]),
+                 lambda: B.moe_dropout_fwd(x, 0.1, rng),
+                 lambda: B.moe_dropout_fwd(x, 0.1, rng.int()),
+                 lambda: B.moe_dropout_fwd(x.t(), 0.1, rng),
+                 lambda: B.moe_dropout_fwd(x, 0.1, rng, residual=x[:2])):
+        with pytest.raises(B.MoEError):
+            call()
