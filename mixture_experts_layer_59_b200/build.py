@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmoe_b200.so")
 
 SOURCES = ["api.cu", "dropout.cu", "ep.cu", "mx.cu", "norm.cu", "route_permute.cu", "rowops.cu", "simt.cu",
            "tc_gemm.cu"]
-HEADERS = ["common.cuh", "internal.h", "mx.cuh", "tcgen05.cuh"]
+HEADERS = ["common.cuh", "internal.h", "mx.cuh", "tc_tile.cuh", "tcgen05.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
