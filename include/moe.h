@@ -509,6 +509,36 @@ int moe_dropout_bwd(const void* dout, int64_t n, double p, const int64_t* rng, i
                     void* stream);
 
 /*
+ * moe_shared_ffn_fwd -- the dense (shared) gated feed-forward expert that
+ *   every token passes, next to the routed ones; SwiGLU as theirs:
+ *   H = [x W1 | x W3], A = silu(H1) * H3 (one kernel), y = A W2 + addend.
+ *   x [T,d]; w1, w3 [d,f]; w2 [f,d]; addend [T,d] (the routed experts'
+ *   output, joined in the last product's epilogue) or NULL; H [T,2f] out, for
+ *   the backward pass, or NULL (serving: not written); y [T,d] out; y may be
+ *   addend itself.  bf16 only, fp32 accumulation, H and A each rounded
+ *   once to bf16 (A from the unrounded H).  T >= 0; d and f multiples of 8 (<= 2^20); all pointers 16-byte
+ *   aligned.  ws: at least moe_shared_ffn_fwd_workspace_size() bytes.  Needs
+ *   an sm_100 device.
+ * moe_shared_ffn_bwd -- from dout and the saved x and H, with A recomputed:
+ *   dA = dout W2^T, dH = [dA*H3*silu'(H1) | dA*silu(H1)],
+ *   dx = dH [W1 | W3]^T + addend (addend [T,d], e.g. the routed experts' dx,
+ *   or NULL; dx may be addend itself), dW1 = x^T dH1, dW3 = x^T dH3,
+ *   dW2 = A^T dout, all bf16 and overwritten (no accumulation; zeros when
+ *   T = 0).  ws: at least moe_shared_ffn_bwd_workspace_size() bytes.
+ * Sums run in a fixed order (deterministic).  Outputs must not overlap other
+ * inputs than named above.
+ */
+size_t moe_shared_ffn_fwd_workspace_size(int T, int d, int f, int dtype);
+int moe_shared_ffn_fwd(const void* x, const void* w1, const void* w3, const void* w2,
+                       const void* addend, int T, int d, int f, int dtype, void* H, void* y,
+                       void* ws, size_t ws_bytes, void* stream);
+size_t moe_shared_ffn_bwd_workspace_size(int T, int d, int f, int dtype);
+int moe_shared_ffn_bwd(const void* dout, const void* x, const void* w1, const void* w3,
+                       const void* w2, const void* H, const void* addend, int T, int d, int f,
+                       int dtype, void* dx, void* dw1, void* dw3, void* dw2, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
  * moe_check_status -- synchronises `stream`, then reads and clears the
  * device status word of the current device.  Returns MOE_OK, MOE_ERR_CUDA
  * (a CUDA error), MOE_ERR_DEVICE_TIMEOUT if a bounded device wait expired

@@ -36,7 +36,8 @@ EXPORTS = [
     "moe_ep_receive_plan", "moe_expert_rows_fwd_workspace_size", "moe_expert_rows_fwd",
     "moe_expert_rows_bwd_workspace_size", "moe_expert_rows_bwd", "moe_token_bwd_workspace_size",
     "moe_token_bwd", "moe_layernorm_fwd", "moe_layernorm_bwd_workspace_size", "moe_layernorm_bwd",
-    "moe_dropout_fwd", "moe_dropout_bwd",
+    "moe_dropout_fwd", "moe_dropout_bwd", "moe_shared_ffn_fwd_workspace_size",
+    "moe_shared_ffn_fwd", "moe_shared_ffn_bwd_workspace_size", "moe_shared_ffn_bwd",
 ]
 
 _lib = None
@@ -94,6 +95,10 @@ _SIGS = {
                           + [_sz, _vp]),
     "moe_dropout_fwd": (_i, [_vp, _vp, _i64, _d, _vp, _i, _vp, _vp]),
     "moe_dropout_bwd": (_i, [_vp, _i64, _d, _vp, _i, _vp, _vp]),
+    "moe_shared_ffn_fwd_workspace_size": (_sz, [_i] * 4),
+    "moe_shared_ffn_fwd": (_i, [_vp] * 5 + [_i] * 4 + [_vp] * 3 + [_sz, _vp]),
+    "moe_shared_ffn_bwd_workspace_size": (_sz, [_i] * 4),
+    "moe_shared_ffn_bwd": (_i, [_vp] * 7 + [_i] * 4 + [_vp] * 5 + [_sz, _vp]),
 }
 
 
@@ -682,3 +687,67 @@ def moe_dropout_bwd(dout, p, rng, dx=None, stream=None):
         _check(lib().moe_dropout_bwd(dout.data_ptr(), dout.numel(), p, rng.data_ptr(), dt,
                                      dx.data_ptr(), s))
     return dx
+
+
+def _check_ffn(x, w1, w3, w2):
+    if x.dim() != 2 or w1.dim() != 2:
+        _bad("x and w1: expected matrices")
+    (T, d), f = x.shape, w1.shape[1]
+    dev, dt = x.device, _code("x", x)
+    for name, t, shape in (("x", x, (T, d)), ("w1", w1, (d, f)), ("w3", w3, (d, f)),
+                           ("w2", w2, (f, d))):
+        _check_arg(name, t, shape, x.dtype, dev)
+    return T, d, f, dev, dt
+
+
+def moe_shared_ffn_fwd(x, w1, w3, w2, addend=None, H=None, y=None, save=True, ws=None,
+                       stream=None):
+    """Dense gated FFN: returns (y [T, d] = A W2 + addend, H [T, 2f]); save
+    False: H is not written and None is returned for it (serving)."""
+    T, d, f, dev, dt = _check_ffn(x, w1, w3, w2)
+    if addend is not None:
+        _check_arg("addend", addend, (T, d), x.dtype, dev)
+    with _On(dev, stream) as s:
+        if not save:
+            H = None
+        elif H is None:
+            H = torch.empty(T, 2 * f, device=dev, dtype=x.dtype)
+        else:
+            _check_arg("H", H, (T, 2 * f), x.dtype, dev)
+        if y is None:
+            y = torch.empty(T, d, device=dev, dtype=x.dtype)
+        else:
+            _check_arg("y", y, (T, d), x.dtype, dev)
+        if ws is None:
+            ws = torch.empty(max(lib().moe_shared_ffn_fwd_workspace_size(T, d, f, dt), 1),
+                             device=dev, dtype=torch.uint8)
+        _check(lib().moe_shared_ffn_fwd(x.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
+                                        _ptr(addend), T, d, f, dt, _ptr(H), y.data_ptr(),
+                                        ws.data_ptr(), ws.numel(), s))
+    return y, H
+
+
+def moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend=None, out=None, ws=None, stream=None):
+    """Backward of moe_shared_ffn_fwd.  Returns dict dx [T, d] (+ addend),
+    dw1, dw3 [d, f], dw2 [f, d]."""
+    T, d, f, dev, dt = _check_ffn(x, w1, w3, w2)
+    _check_arg("dout", dout, (T, d), x.dtype, dev)
+    _check_arg("H", H, (T, 2 * f), x.dtype, dev)
+    if addend is not None:
+        _check_arg("addend", addend, (T, d), x.dtype, dev)
+    o = dict(out) if out else {}
+    with _On(dev, stream) as s:
+        for name, shape in (("dx", (T, d)), ("dw1", (d, f)), ("dw3", (d, f)), ("dw2", (f, d))):
+            if name not in o:
+                o[name] = torch.empty(shape, device=dev, dtype=x.dtype)
+            else:
+                _check_arg(name, o[name], shape, x.dtype, dev)
+        if ws is None:
+            ws = torch.empty(max(lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dt), 1),
+                             device=dev, dtype=torch.uint8)
+        _check(lib().moe_shared_ffn_bwd(dout.data_ptr(), x.data_ptr(), w1.data_ptr(),
+                                        w3.data_ptr(), w2.data_ptr(), H.data_ptr(), _ptr(addend),
+                                        T, d, f, dt, o["dx"].data_ptr(), o["dw1"].data_ptr(),
+                                        o["dw3"].data_ptr(), o["dw2"].data_ptr(), ws.data_ptr(),
+                                        ws.numel(), s))
+    return o

@@ -19,8 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 
-SOURCES = ["api.cu", "dropout.cu", "ep.cu", "mx.cu", "norm.cu", "route_permute.cu", "rowops.cu", "simt.cu",
-           "tc_gemm.cu"]
+SOURCES = ["api.cu", "dropout.cu", "ep.cu", "ffn.cu", "mx.cu", "norm.cu", "route_permute.cu", "rowops.cu",
+           "simt.cu", "tc_gemm.cu"]
 HEADERS = ["common.cuh", "internal.h", "mx.cuh", "tc_tile.cuh", "tcgen05.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

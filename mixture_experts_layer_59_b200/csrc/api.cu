@@ -217,6 +217,21 @@ struct TokenBwdWs {
   }
 };
 
+template <class A>
+struct SharedFwdWs {
+  uint16_t* act = nullptr;
+  void carve(A& a, int T, int f) { act = a.template take<uint16_t>((size_t)T * f); }
+};
+
+template <class A>
+struct SharedBwdWs {
+  uint16_t *dH = nullptr, *act = nullptr;
+  void carve(A& a, int T, int f) {
+    dH = a.template take<uint16_t>((size_t)T * 2 * f);
+    act = a.template take<uint16_t>((size_t)T * f);
+  }
+};
+
 }  // namespace moe
 
 using namespace moe;
@@ -922,6 +937,80 @@ int moe_dropout_fwd(const void* x, const void* residual, int64_t n, double p, co
 int moe_dropout_bwd(const void* dout, int64_t n, double p, const int64_t* rng, int dtype, void* dx,
                     void* stream) {
   return dropout_checked(dout, nullptr, n, p, rng, dtype, dx, "dropout_bwd", stream);
+}
+
+// ------------------------------------------------------------ shared gated FFN
+static int check_ffn(int T, int d, int f, int dtype) {
+  if (dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "the shared FFN takes MOE_BF16 only");
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0");
+  if (d <= 0 || d % 8) return fail(MOE_ERR_UNSUPPORTED, "d must be a positive multiple of 8");
+  if (f <= 0 || f % 8) return fail(MOE_ERR_UNSUPPORTED, "f must be a positive multiple of 8");
+  if (d > (1 << 20) || f > (1 << 20) || T > (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "d and f must be <= 2^20, T <= 2^30");
+  if (!tc_available()) return fail(MOE_ERR_UNSUPPORTED, "the shared FFN needs an sm_100 device");
+  return MOE_OK;
+}
+
+size_t moe_shared_ffn_fwd_workspace_size(int T, int d, int f, int dtype) {
+  if (T <= 0 || d <= 0 || f <= 0 || dtype != MOE_BF16) return 0;
+  Sizer z;
+  SharedFwdWs<Sizer> w;
+  w.carve(z, T, f);
+  return z.used;
+}
+
+int moe_shared_ffn_fwd(const void* x, const void* w1, const void* w3, const void* w2,
+                       const void* addend, int T, int d, int f, int dtype, void* H, void* y,
+                       void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_ffn(T, d, f, dtype)) return rc;
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(w1); REQUIRE_PTR(w3); REQUIRE_PTR(w2); REQUIRE_PTR(y);
+  REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w1); REQUIRE_ALIGNED(w3); REQUIRE_ALIGNED(w2);
+  REQUIRE_ALIGNED(addend); REQUIRE_ALIGNED(H); REQUIRE_ALIGNED(y);
+  REQUIRE_PTR(ws);
+  REQUIRE_ALIGNED(ws);
+  Carve c(ws, ws_bytes);
+  SharedFwdWs<Carve> w;
+  w.carve(c, T, f);
+  if (!c.ok)
+    return fail(MOE_ERR_WORKSPACE, "shared FFN workspace smaller than moe_shared_ffn_fwd_workspace_size()");
+  return ffn_fwd(FfnDense{x, w1, w3, w2, T, d, f}, addend, H, w.act, y, (cudaStream_t)stream);
+}
+
+size_t moe_shared_ffn_bwd_workspace_size(int T, int d, int f, int dtype) {
+  if (T <= 0 || d <= 0 || f <= 0 || dtype != MOE_BF16) return 0;
+  Sizer z;
+  SharedBwdWs<Sizer> w;
+  w.carve(z, T, f);
+  return z.used;
+}
+
+int moe_shared_ffn_bwd(const void* dout, const void* x, const void* w1, const void* w3,
+                       const void* w2, const void* H, const void* addend, int T, int d, int f,
+                       int dtype, void* dx, void* dw1, void* dw3, void* dw2, void* ws,
+                       size_t ws_bytes, void* stream) {
+  if (int rc = check_ffn(T, d, f, dtype)) return rc;
+  REQUIRE_PTR(dw1); REQUIRE_PTR(dw3); REQUIRE_PTR(dw2);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (T == 0) {   // no rows: the sums over them are zero
+    for (void* g : {dw1, dw3, dw2})
+      if (cudaError_t e = cudaMemsetAsync(g, 0, (size_t)2 * d * f, s))
+        return cuda_fail(e, "shared_ffn_bwd zero gradients");
+    return MOE_OK;
+  }
+  REQUIRE_PTR(dout); REQUIRE_PTR(x); REQUIRE_PTR(w1); REQUIRE_PTR(w3); REQUIRE_PTR(w2);
+  REQUIRE_PTR(H); REQUIRE_PTR(dx);
+  REQUIRE_ALIGNED(dout); REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w1); REQUIRE_ALIGNED(w3);
+  REQUIRE_ALIGNED(w2); REQUIRE_ALIGNED(H); REQUIRE_ALIGNED(addend); REQUIRE_ALIGNED(dx);
+  REQUIRE_ALIGNED(dw1); REQUIRE_ALIGNED(dw3); REQUIRE_ALIGNED(dw2);
+  REQUIRE_PTR(ws);
+  REQUIRE_ALIGNED(ws);
+  Carve c(ws, ws_bytes);
+  SharedBwdWs<Carve> w;
+  w.carve(c, T, f);
+  if (!c.ok)
+    return fail(MOE_ERR_WORKSPACE, "shared FFN workspace smaller than moe_shared_ffn_bwd_workspace_size()");
+  return ffn_bwd(FfnDense{x, w1, w3, w2, T, d, f}, dout, H, addend, w.dH, w.act, dx, dw1, dw3, dw2, s);
 }
 
 int moe_check_status(void* stream) {

@@ -126,6 +126,17 @@ int launch_ds_rows(const float* ds_part, int nparts, const int32_t* offsets, int
 // the next tensor-core GEMM launch, or 0; taking it clears the request.
 long long take_debug_expire();
 
+// ---------------------------------------------------------------- shared FFN (ffn.cu)
+struct FfnDense {
+  const void *x, *w1, *w3, *w2;   // [T, d], [d, f], [d, f], [f, d] bf16
+  int T, d, f;
+};
+// H [T, 2f] or null; act [T, f] workspace; addend [T, d] or null.
+int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, cudaStream_t s);
+// dH [T, 2f] and act [T, f]: workspace.
+int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* addend, void* dH,
+            void* act, void* dx, void* dw1, void* dw3, void* dw2, cudaStream_t s);
+
 // ---------------------------------------------------------------- layer norm (norm.cu)
 int launch_layernorm_fwd(const void* x, int64_t ldx, const void* w, const void* b, int T, int d,
                          int dtype, int wdtype, float eps, void* y, float* mean, float* rstd,

@@ -116,14 +116,15 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 row-major [outer, inner] viewed in boxes of box_outer x box_inner.
+// bf16 row-major [outer, inner] (rows ld elements apart; 0: inner) viewed in
+// boxes of box_outer x box_inner.
 inline int make_map_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
                        uint32_t box_inner, uint32_t box_outer,
-                       CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+                       CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, uint64_t ld = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * 2};
+  cuuint64_t strides[1] = {(ld ? ld : inner) * 2};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t es[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides,
@@ -155,18 +156,20 @@ inline int make_store_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint6
   return make_map_2d(m, ptr, inner, outer, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// bf16 [batch, outer, inner] (inner contiguous, a multiple of 64) as the
+// bf16 [batch, outer, inner] (inner contiguous, a multiple of 64; rows ld
+// elements apart, 0: inner) as the
 // 4-d view [batch][inner / 64][outer][64]: one box brings `atoms` adjacent
 // 64-column blocks of BK rows, stored block after block (BK x 128 bytes
 // each, 128-byte swizzle) -- the shared-memory layout of an MN-major
 // operand -- so a stage's operand takes one copy instead of one per block.
 inline int make_map_atoms(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
-                          uint64_t batch, uint32_t atoms) {
+                          uint64_t batch, uint32_t atoms, uint64_t ld = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   if (inner % 64 != 0) return fail(MOE_ERR_INVALID_ARG, "operand width not a multiple of 64");
   cuuint64_t dims[4] = {64, outer, inner / 64, batch};
-  cuuint64_t strides[3] = {inner * 2, 128, inner * outer * 2};
+  if (ld == 0) ld = inner;
+  cuuint64_t strides[3] = {ld * 2, 128, ld * outer * 2};
   cuuint32_t box[4] = {64, (cuuint32_t)BK, atoms, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides,

@@ -72,3 +72,52 @@ def test_binding_refuses_what_it_cannot_launch():
                  lambda: B.moe_dropout_fwd(x, 0.1, rng, residual=x[:2])):
         with pytest.raises(B.MoEError):
             call()
+
+
+def ffn_fwd(**kw):
+    a = dict(x=F, w1=F, w3=F, w2=F, add=None, T=4, d=256, f=128, dt=B.MOE_BF16, H=F, y=F, ws=F, wsb=1 << 30)
+    a.update(kw)
+    return B.lib().moe_shared_ffn_fwd(*a.values(), None)
+
+
+def ffn_bwd(**kw):
+    a = dict(dout=F, x=F, w1=F, w3=F, w2=F, H=F, add=None, T=4, d=256, f=128, dt=B.MOE_BF16, dx=F, dw1=F, dw3=F,
+             dw2=F, ws=F, wsb=1 << 30)
+    a.update(kw)
+    return B.lib().moe_shared_ffn_bwd(*a.values(), None)
+
+
+SHARED = [(dict(dt=B.MOE_F32), -2), (dict(T=-1), -1), (dict(d=12), -2), (dict(f=4), -2), (dict(d=0), -2),
+          (dict(f=-8), -2), (dict(d=1 << 21), -2), (dict(x=None), -1), (dict(w1=None), -1), (dict(w3=None), -1),
+          (dict(w2=None), -1), (dict(x=ctypes.c_void_p(264)), -1), (dict(w2=ctypes.c_void_p(258)), -1),
+          (dict(add=ctypes.c_void_p(258)), -1), (dict(ws=None), -1), (dict(wsb=8), -5)]
+
+
+@pytest.mark.parametrize("kw,code", SHARED + [(dict(y=None), -1), (dict(H=ODD), -1), (dict(T=0, x=None, y=None), 0)])
+def test_shared_ffn_fwd_refusals(kw, code):
+    assert ffn_fwd(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", SHARED + [(dict(dout=None), -1), (dict(H=None), -1), (dict(dx=None), -1),
+                                              (dict(dw2=None), -1), (dict(dw1=ODD), -1)])
+def test_shared_ffn_bwd_refusals(kw, code):
+    assert ffn_bwd(**kw) == code
+
+
+def test_shared_ffn_workspaces():
+    for size in (B.lib().moe_shared_ffn_fwd_workspace_size, B.lib().moe_shared_ffn_bwd_workspace_size):
+        assert size(0, 256, 128, B.MOE_BF16) == 0 and size(10, 256, 128, B.MOE_F32) == 0
+        assert 0 < size(10, 256, 128, B.MOE_BF16) < size(10000, 256, 128, B.MOE_BF16)
+
+
+def test_binding_refuses_ffn_arguments():
+    bf = torch.bfloat16
+    x, w1, w2 = torch.zeros(4, 16, dtype=bf), torch.zeros(16, 8, dtype=bf), torch.zeros(8, 16, dtype=bf)
+    for call in (lambda: B.moe_shared_ffn_fwd(x, w1, w1, w2),                   # not on a CUDA device
+                 lambda: B.moe_shared_ffn_fwd(x, w1, w2, w2),                   # shape
+                 lambda: B.moe_shared_ffn_fwd(x, w1, w1, w1.t()),               # not contiguous
+                 lambda: B.moe_shared_ffn_fwd(x.float(), w1, w1, w2),           # types differ
+                 lambda: B.moe_shared_ffn_fwd(x, w1, w1, w2, addend=x[:2]),
+                 lambda: B.moe_shared_ffn_bwd(x, x, w1, w1, w2, torch.zeros(4, 8, dtype=bf))):
+        with pytest.raises(B.MoEError):
+            call()
