@@ -220,15 +220,21 @@ struct TokenBwdWs {
 template <class A>
 struct SharedFwdWs {
   uint16_t* act = nullptr;
-  void carve(A& a, int T, int f) { act = a.template take<uint16_t>((size_t)T * f); }
+  char* scratch = nullptr;
+  void carve(A& a, int T, int d, int f) {
+    act = a.template take<uint16_t>((size_t)T * f);
+    scratch = a.template take<char>(ffn_scratch_bytes(T, d, f, false));
+  }
 };
 
 template <class A>
 struct SharedBwdWs {
   uint16_t *dH = nullptr, *act = nullptr;
-  void carve(A& a, int T, int f) {
+  char* scratch = nullptr;
+  void carve(A& a, int T, int d, int f) {
     dH = a.template take<uint16_t>((size_t)T * 2 * f);
     act = a.template take<uint16_t>((size_t)T * f);
+    scratch = a.template take<char>(ffn_scratch_bytes(T, d, f, true));
   }
 };
 
@@ -955,7 +961,7 @@ size_t moe_shared_ffn_fwd_workspace_size(int T, int d, int f, int dtype) {
   if (T <= 0 || d <= 0 || f <= 0 || dtype != MOE_BF16) return 0;
   Sizer z;
   SharedFwdWs<Sizer> w;
-  w.carve(z, T, f);
+  w.carve(z, T, d, f);
   return z.used;
 }
 
@@ -971,17 +977,18 @@ int moe_shared_ffn_fwd(const void* x, const void* w1, const void* w3, const void
   REQUIRE_ALIGNED(ws);
   Carve c(ws, ws_bytes);
   SharedFwdWs<Carve> w;
-  w.carve(c, T, f);
+  w.carve(c, T, d, f);
   if (!c.ok)
     return fail(MOE_ERR_WORKSPACE, "shared FFN workspace smaller than moe_shared_ffn_fwd_workspace_size()");
-  return ffn_fwd(FfnDense{x, w1, w3, w2, T, d, f}, addend, H, w.act, y, (cudaStream_t)stream);
+  return ffn_fwd(FfnDense{x, w1, w3, w2, T, d, f}, addend, H, w.act, y, w.scratch,
+                 (cudaStream_t)stream);
 }
 
 size_t moe_shared_ffn_bwd_workspace_size(int T, int d, int f, int dtype) {
   if (T <= 0 || d <= 0 || f <= 0 || dtype != MOE_BF16) return 0;
   Sizer z;
   SharedBwdWs<Sizer> w;
-  w.carve(z, T, f);
+  w.carve(z, T, d, f);
   return z.used;
 }
 
@@ -1007,10 +1014,11 @@ int moe_shared_ffn_bwd(const void* dout, const void* x, const void* w1, const vo
   REQUIRE_ALIGNED(ws);
   Carve c(ws, ws_bytes);
   SharedBwdWs<Carve> w;
-  w.carve(c, T, f);
+  w.carve(c, T, d, f);
   if (!c.ok)
     return fail(MOE_ERR_WORKSPACE, "shared FFN workspace smaller than moe_shared_ffn_bwd_workspace_size()");
-  return ffn_bwd(FfnDense{x, w1, w3, w2, T, d, f}, dout, H, addend, w.dH, w.act, dx, dw1, dw3, dw2, s);
+  return ffn_bwd(FfnDense{x, w1, w3, w2, T, d, f}, dout, H, addend, w.dH, w.act, dx, dw1, dw3, dw2,
+                 w.scratch, s);
 }
 
 int moe_check_status(void* stream) {

@@ -32,7 +32,11 @@ struct FfnArgs {
   int T, d, f;
   int M[3], N[3];      // output rows and columns (UP: N counts the W1 columns)
   int mtiles[3], ntiles[3];
-  int tile0, tiles;    // this launch: output tiles tile0 .. tiles - 1
+  int tiles;           // output tiles
+  int whole, parts;    // pairs: tiles below `whole` are computed by one pair, the
+                       // others by `parts` pairs along K each
+  float4* part;        // pairs: fp32 partials [split tile * parts + p][rank][PART4]
+  int* count;          // pairs: arrivals [split tile][rank], zero at the start
   int kbs, kbh;        // k-blocks per tile; DX: of them with dH1
   int a4, b4;          // operand widths are multiples of 64: one box per stage
   int save_h;          // UP: write H
@@ -56,21 +60,20 @@ template <int BN> struct FCfg {
   static constexpr int B_BYTES = BN * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = BN == 256 ? 4 : 6;
-  static constexpr int OUT_BYTES = 8 * 2 * 2048;
-  static constexpr int SMEM = STAGES * STAGE + OUT_BYTES;
-  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int SMEM = STAGES * STAGE;
+  static constexpr int TMEM_COLS = BN;
   static_assert(STAGE % 1024 == 0, "stages must keep 1 KB alignment");
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(BM * BN * 4 <= SMEM && SMEM <= 227 * 1024, "partials reuse the stages");
 };
 
 struct FTile {
   int p, m0, n0;
 };
 
-// Tiles in groups of 16 row tiles, columns outside rows within a group: the
-// 148 tiles in flight then cover about as many rows as columns, and both
-// operands' share of them stays in L2.
-template <int KIND, int BN>
+// Tiles of ROWS x BN in groups of 2048 rows, columns outside rows within a
+// group: the tiles in flight then cover about as many rows as columns, and
+// both operands' share of them stays in L2.
+template <int KIND, int BN, int ROWS>
 __device__ __forceinline__ FTile f_tile(int t, const FfnArgs& a) {
   FTile ti;
   ti.p = 0;
@@ -80,10 +83,10 @@ __device__ __forceinline__ FTile f_tile(int t, const FfnArgs& a) {
       ++ti.p;
     }
   }
-  constexpr int GM = 16;
+  constexpr int GM = 2048 / ROWS;
   const int nt = a.ntiles[ti.p], per = GM * nt, g = t / per, r = t - g * per;
   const int gs = min(GM, a.mtiles[ti.p] - g * GM);
-  ti.m0 = (g * GM + r % gs) * BM;
+  ti.m0 = (g * GM + r % gs) * ROWS;
   ti.n0 = (r / gs) * (KIND == F_UP ? BN / 2 : BN);
   return ti;
 }
@@ -97,6 +100,17 @@ __device__ __forceinline__ void load_mn(uint8_t* dst, const CUtensorMap* m, uint
   } else {
 #pragma unroll
     for (int i = 0; i < ATOMS; ++i) tma_load_2d(dst + i * ATOM, m, bar, c0 + 64 * i, k0);
+  }
+}
+
+// The same for one CTA of a pair (two 64-column blocks).
+__device__ __forceinline__ void load_mn_pair(uint8_t* dst, const CUtensorMap* m, uint32_t bar,
+                                             int k0, int c0, bool one_box) {
+  if (one_box) {
+    tma_load_4d_pair(dst, m, bar, 0, k0, c0 / 64, 0);
+  } else {
+    tma_load_2d_pair(dst, m, bar, c0, k0);
+    tma_load_2d_pair(dst + ATOM, m, bar, c0 + 64, k0);
   }
 }
 
@@ -141,17 +155,15 @@ __device__ __forceinline__ void part_sum8(uint32_t base, int nranks, int row, in
   }
 }
 
-// SPLIT: the CTAs of a cluster share one tile, each takes a slice of its
-// k-blocks, and the partial sums meet in distributed shared memory: for the
-// tiles that do not fill the SMs (few rows, or the last wave of many).
-template <int KIND, int BN, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnArgs a) {
+// Few rows: the CTAs of a cluster share one 128 x BN tile, each takes a slice
+// of its k-blocks, and the partial sums meet in distributed shared memory.
+template <int KIND, int BN>
+__global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant__ FfnArgs a) {
   using C = FCfg<BN>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[C::STAGES];
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
-  __shared__ __align__(8) uint64_t tfull_bar[2];
-  __shared__ __align__(8) uint64_t tempty_bar[2];
+  __shared__ __align__(8) uint64_t tfull_bar;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -165,10 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&tfull_bar[s], 1);
-      mbar_init(&tempty_bar[s], EPI_THREADS);
-    }
+    mbar_init(&tfull_bar, 1);
     fence_mbar_init();
     prefetch_tmap(&a.mA[0]);
     prefetch_tmap(&a.mB[0]);
@@ -183,22 +192,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
   const uint32_t tmem_base = s_tmem;
   grid_dependency_wait();      // the previous product's results
   grid_launch_dependents();
-  const int nranks = SPLIT ? (int)cluster_size() : 1, rank = SPLIT ? (int)cluster_rank() : 0;
-  const int t_first = a.tile0 + (SPLIT ? (int)blockIdx.x / nranks : (int)blockIdx.x);
-  const int t_end = SPLIT ? t_first + 1 : a.tiles, t_step = SPLIT ? 1 : (int)gridDim.x;
-  const int kb_begin = SPLIT ? (int)((int64_t)a.kbs * rank / nranks) : 0;
-  const int kb_end = SPLIT ? (int)((int64_t)a.kbs * (rank + 1) / nranks) : a.kbs;
+  const int nranks = (int)cluster_size(), rank = (int)cluster_rank();
+  const FTile ti = f_tile<KIND, BN, BM>((int)blockIdx.x / nranks, a);
+  const int kb_begin = (int)((int64_t)a.kbs * rank / nranks);
+  const int kb_end = (int)((int64_t)a.kbs * (rank + 1) / nranks);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0 && !a.dbg_no_load) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int t = t_first; t < t_end; t += t_step) {
-        const FTile ti = f_tile<KIND, BN>(t, a);
         for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (!bounded_wait(&empty_bar[stage], phase ^ 1, &s_abort, a.status, 1, a.wait_ns))
-            goto producer_done;
+          if (!bounded_wait(&empty_bar[stage], phase ^ 1, &s_abort, a.status, 1, a.wait_ns)) break;
           uint8_t* sA = smem + stage * C::STAGE;
           uint8_t* sB = sA + A_BYTES;
           uint64_t* bar = &full_bar[stage];
@@ -225,8 +230,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
           }
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
-      }
-    producer_done:;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -234,14 +237,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
       constexpr uint32_t IDESC = idesc_bf16(BM, BN, FK<KIND>::A_MN, FK<KIND>::B_MN);
       int stage = 0;
       uint32_t phase = 0;
-      int it = 0;
-      for (int t = t_first; t < t_end; t += t_step, ++it) {
-        const int acc = it & 1;
-        if (!bounded_wait(&tempty_bar[acc], ((it >> 1) & 1) ^ 1, &s_abort, a.status, 2, a.wait_ns)) break;
-        fence_after_sync();
-        const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (!bounded_wait(&full_bar[stage], phase, &s_abort, a.status, 3, a.wait_ns)) goto mma_done;
+          if (!bounded_wait(&full_bar[stage], phase, &s_abort, a.status, 3, a.wait_ns)) break;
           fence_after_sync();
           const uint32_t sA = smem_u32(smem + stage * C::STAGE);
           const uint32_t sB = sA + A_BYTES;
@@ -251,14 +248,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
                                                : sdesc_sw128(sA + ks * 32, 16, 1024);
             const uint64_t bd = FK<KIND>::B_MN ? sdesc_sw128(sB + ks * 2048, ATOM, 1024)
                                                : sdesc_sw128(sB + ks * 32, 16, 1024);
-            umma_bf16(d_tmem, ad, bd, IDESC, kb > kb_begin || ks > 0);
+            umma_bf16(tmem_base, ad, bd, IDESC, kb > kb_begin || ks > 0);
           }
           umma_commit(&empty_bar[stage]);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
-        umma_commit(&tfull_bar[acc]);
-      }
-    mma_done:;
+      umma_commit(&tfull_bar);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -266,132 +261,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
     const int half = (warp - 2) >> 2;            // which half of the tile's columns
     const int rloc = q * 32 + lane;              // row of the tile owned by this thread
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-    if constexpr (SPLIT) {
-      // this slice's partial, fp32, over the pipeline's stages: every copy
-      // into them has landed and every MMA that reads them is done
-      const FTile ti = f_tile<KIND, BN>(t_first, a);
-      if (bounded_wait(&tfull_bar[0], 0, &s_abort, a.status, 4, a.wait_ns) &&
-          ti.m0 + q * 32 < a.M[ti.p]) {
-        fence_after_sync();
+    // this slice's partial, fp32, over the pipeline's stages: every copy into
+    // them has landed and every MMA that reads them is done
+    if (bounded_wait(&tfull_bar, 0, &s_abort, a.status, 4, a.wait_ns) &&
+        ti.m0 + q * 32 < a.M[ti.p]) {
+      fence_after_sync();
 #pragma unroll 1
-        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-          uint32_t r[32];
-          tmem_ld32(tlane + c, r);
-          tmem_ld_wait();
+      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tlane + c, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(smem + part_off<BN>(rloc, c / 4 + i)) =
-                make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-        }
-      }
-    } else {
-      uint8_t* otile = smem + C::STAGES * C::STAGE + (warp - 2) * 4096;
-      int obuf = 0;
-      int it = 0;
-      // what the epilogue reads of memory (H; the addend) is loaded ahead in
-      // 32-column chunks, across tiles: PRE chunks before they are needed
-      constexpr int CH = (KIND == F_UP ? BN / 4 : BN / 2) / 32;   // chunks of a tile per warp
-      constexpr int PRE = KIND == F_DAP ? 2 : CH;
-      constexpr bool RD1 = KIND == F_DAP || KIND == F_DOWN || KIND == F_DX;
-      uint4 n1[RD1 ? PRE : 1][4], n3[KIND == F_DAP ? PRE : 1][4];
-      const bool rd = KIND == F_DAP || (RD1 && a.addend != nullptr);
-      auto fetch = [&](int t, int j, int slot) {   // chunk j of tile t
-        if (t >= t_end) return;
-        const FTile ti = f_tile<KIND, BN>(t, a);
-        const int row = ti.m0 + rloc, col = ti.n0 + (half * CH + j) * 32;
-        const bool live = row < a.M[0];
-        if constexpr (KIND == F_DAP) {
-          const __nv_bfloat16* rp = a.hin + (size_t)row * 2 * a.f;
-          ld_row32(rp, col, a.N[0], live, n1[slot]);
-          ld_row32(rp + a.f, col, a.N[0], live, n3[slot]);
-        } else if constexpr (RD1) {
-          ld_row32(a.addend + (size_t)row * a.N[0], col, a.N[0], live, n1[slot]);
-        }
-      };
-      if (rd) {
-#pragma unroll
-        for (int j = 0; j < PRE; ++j) fetch(t_first, j, j);
-      }
-      for (int t = t_first; t < t_end; t += t_step, ++it) {
-        const FTile ti = f_tile<KIND, BN>(t, a);
-        const int acc = it & 1;
-        const int row0 = ti.m0 + q * 32;
-        const int M = a.M[ti.p], N = a.N[ti.p];
-        if (!bounded_wait(&tfull_bar[acc], (it >> 1) & 1, &s_abort, a.status, 4, a.wait_ns)) break;
-        fence_after_sync();
-        const uint32_t tbase = tlane + acc * BN;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const int c = (half * CH + j) * 32, col = ti.n0 + c;
-          const bool inside = col < N && row0 < M;   // else the whole box lies outside
-          float v[32];
-          uint32_t r[32];
-          tmem_ld32(tbase + c, r);
-          if constexpr (KIND == F_UP) {
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            float h3[32];
-            tmem_ld32(tbase + BN / 2 + c, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) h3[i] = __uint_as_float(r[i]);
-            if (!inside) continue;
-            if (a.save_h) {
-              stage_store(otile, obuf, v, &a.sO[0], col, row0, lane);
-              stage_store(otile, obuf, h3, &a.sO[1], col, row0, lane);
-            }
-            // A from the accumulator, not from the rounded H: one rounding less
-            // between x and y (2-norm error of y 2.4e-3 instead of 3.1e-3)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * h3[i];
-            stage_store(otile, obuf, v, &a.sO[2], col, row0, lane);
-          } else if constexpr (KIND == F_DAP) {
-            tmem_ld_wait();
-            float d3[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float h1 = bf16_lane(n1[j % PRE], i), h3 = bf16_lane(n3[j % PRE], i);
-              const float da = __uint_as_float(r[i]);
-              const float sg = sigmoid_fast(h1);
-              const float sl = h1 * sg;
-              v[i] = da * h3 * (sg * (1.0f + h1 * (1.0f - sg)));
-              d3[i] = da * sl;
-              r[i] = __float_as_uint(sl * h3);
-            }
-            if (j + PRE < CH) fetch(t, j + PRE, j % PRE);
-            else fetch(t + t_step, j + PRE - CH, j % PRE);
-            if (!inside) continue;
-            stage_store(otile, obuf, v, &a.sO[0], col, row0, lane);
-            stage_store(otile, obuf, d3, &a.sO[1], col, row0, lane);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            stage_store(otile, obuf, v, &a.sO[2], col, row0, lane);
-          } else {
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            if constexpr (RD1) {
-              if (rd) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += bf16_lane(n1[j], i);
-                fetch(t + t_step, j, j);
-              }
-            }
-            if (!inside) continue;
-            stage_store(otile, obuf, v, &a.sO[KIND == F_DW ? ti.p : 0], col, row0, lane);
-          }
-        }
-        fence_before_sync();
-        mbar_arrive(&tempty_bar[acc]);
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + part_off<BN>(rloc, c / 4 + i)) =
+              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
       }
     }
   }
 
-  if constexpr (SPLIT) {
-    __syncwarp();
-    cluster_sync();            // every partial of the tile is in place
-    const FTile ti = f_tile<KIND, BN>(t_first, a);
+  __syncwarp();
+  cluster_sync();            // every partial of the tile is in place
+  {
     const int M = a.M[ti.p], N = a.N[ti.p];
     const int rows = min(BM, M - ti.m0);
     constexpr int UNITS = (KIND == F_UP ? BN / 2 : BN) / 8;   // 8-column units of a row
@@ -444,10 +334,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
         st_bf16x8(a.out[o] + row * a.ldo[o] + col, v);
       }
     }
-    __syncwarp();
-    cluster_sync();            // no CTA leaves while its partial is still read
   }
-  if (!SPLIT && warp >= 2 && lane == 0) bulk_wait_all();   // the stores end before the CTA does
+  __syncwarp();
+  cluster_sync();            // no CTA leaves while its partial is still read
   if (s_abort) {   // aborted: let copies and MMAs in flight land
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
@@ -460,48 +349,423 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn(const __grid_constant__ FfnA
   }
 }
 
-template <int KIND, int BN, bool SPLIT>
-int f_go(const FfnArgs& a, int grid, int cluster, bool dependent, cudaStream_t s) {
-  using C = FCfg<BN>;
-  static const char* kNames[] = {"ffn_up", "ffn_down", "ffn_dap", "ffn_dx", "ffn_dw"};
-  if (cudaError_t e = cudaFuncSetAttribute(k_ffn<KIND, BN, SPLIT>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM))
+// ============================================================== CTA pairs
+// The kernel of the many-row sizes.  Two CTAs of a cluster share a 256 x 256
+// tile (cta_group::2): each holds 128 rows of A and of the accumulator and
+// half of B's columns, so a k-block brings 32 KB into an SM instead of the
+// 48 KB of a 128 x 256 tile, which the SM's 64 bytes per clock from L2 could
+// not deliver in the 512 clocks the MMAs take.  Persistent; the accumulator is
+// double-buffered in TMEM, six 32 KB stages.
+//
+// The tiles of the last partial wave are cut along K into `parts` units: every
+// unit's epilogue leaves its fp32 partial in global memory (L2), and the unit
+// that arrives last (a counter; nobody waits) adds the others' to its own in
+// part order and runs the epilogue, so the result does not depend on who is
+// last.
+constexpr int PN = 256;                       // tile columns
+constexpr int PSTAGES = 6;
+constexpr int PSTAGE = 2 * A_BYTES;
+constexpr int PSMEM = PSTAGES * PSTAGE + 8 * 2 * 2048;
+constexpr int PART4 = BM * PN / 4;            // float4s of one CTA's partial
+constexpr int MAX_PAIRS = 74;
+
+__device__ __forceinline__ void epi_barrier() {   // the 8 epilogue warps
+  asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+}
+
+struct FUnit {
+  int tile, kb0, kb1, slot;   // slot: partial index, or -1 for a whole tile
+};
+__device__ __forceinline__ FUnit f_unit(int u, const FfnArgs& a) {
+  FUnit w;
+  if (u < a.whole) {
+    w.tile = u;
+    w.kb0 = 0;
+    w.kb1 = a.kbs;
+    w.slot = -1;
+  } else {
+    const int v = u - a.whole, p = v % a.parts;
+    w.tile = a.whole + v / a.parts;
+    w.kb0 = (int)((int64_t)a.kbs * p / a.parts);
+    w.kb1 = (int)((int64_t)a.kbs * (p + 1) / a.parts);
+    w.slot = v;
+  }
+  return w;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__ FfnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full_bar[PSTAGES];    // used in the even CTA: both CTAs' bytes
+  __shared__ __align__(8) uint64_t empty_bar[PSTAGES];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];        // used in the even CTA: both CTAs' warps
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_last;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
+  // 128-byte swizzled tiles need a 1 KB aligned base (the same in every CTA)
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) record_status(a.status, 0x1ff);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int s = 0; s < PSTAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull_bar[s], 1);
+      mbar_init(&tempty_bar[s], 2 * (EPI_THREADS / 32));
+    }
+    fence_mbar_init();
+    prefetch_tmap(&a.mA[0]);
+    prefetch_tmap(&a.mB[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s_tmem, 512);
+    tmem_relinquish_pair();
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();              // the peer's barriers are initialised
+  fence_after_sync();
+  const uint32_t tmem_base = s_tmem;
+  grid_dependency_wait();      // the previous product's results
+  grid_launch_dependents();
+  const int units = a.whole + (a.tiles - a.whole) * a.parts;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0 && !a.dbg_no_load) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int u = pair; u < units; u += npairs) {
+        const FUnit w = f_unit(u, a);
+        FTile ti = f_tile<KIND, PN, 2 * BM>(w.tile, a);
+        const int m0 = ti.m0 + rank * BM;
+        const int n0 = KIND == F_UP ? ti.n0 : ti.n0 + rank * (PN / 2);   // UP: W1 here, W3 there
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!bounded_wait(&empty_bar[stage], phase ^ 1, &s_abort, a.status, 1, a.wait_ns))
+            goto producer_done;
+          uint8_t* sA = smem + stage * PSTAGE;
+          uint8_t* sB = sA + A_BYTES;
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * PSTAGE);
+          const uint32_t bar = map_shared(smem_u32(&full_bar[stage]), 0);
+          const int k0 = kb * BK;
+          if constexpr (KIND == F_DX) {
+            const int h = kb >= a.kbh;
+            const int kk = h ? k0 - a.kbh * BK : k0;
+            tma_load_2d_pair(sA, &a.mA[h], bar, kk, m0);
+            tma_load_2d_pair(sB, &a.mB[h], bar, kk, n0);
+          } else if constexpr (KIND == F_DW) {
+            load_mn_pair(sA, &a.mA[ti.p], bar, k0, m0, (a.a4 >> ti.p) & 1);
+            load_mn_pair(sB, &a.mB[ti.p], bar, k0, n0, (a.b4 >> ti.p) & 1);
+          } else {
+            tma_load_2d_pair(sA, &a.mA[0], bar, k0, m0);
+            if constexpr (KIND == F_DAP) tma_load_2d_pair(sB, &a.mB[0], bar, k0, n0);
+            else load_mn_pair(sB, &a.mB[KIND == F_UP ? rank : 0], bar, k0, n0, a.b4);
+          }
+          if (++stage == PSTAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+    producer_done:;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t IDESC = idesc_bf16(2 * BM, PN, FK<KIND>::A_MN, FK<KIND>::B_MN);
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;
+      for (int u = pair; u < units; u += npairs, ++it) {
+        const FUnit w = f_unit(u, a);
+        const int acc = it & 1;
+        if (!bounded_wait(&tempty_bar[acc], ((it >> 1) & 1) ^ 1, &s_abort, a.status, 2, a.wait_ns)) break;
+        fence_after_sync();
+        const uint32_t d_tmem = tmem_base + acc * PN;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!bounded_wait(&full_bar[stage], phase, &s_abort, a.status, 3, a.wait_ns)) goto mma_done;
+          fence_after_sync();
+          const uint32_t sA = smem_u32(smem + stage * PSTAGE);
+          const uint32_t sB = sA + A_BYTES;
+#pragma unroll
+          for (int ks = 0; ks < BK / 16; ++ks) {
+            const uint64_t ad = FK<KIND>::A_MN ? sdesc_sw128(sA + ks * 2048, ATOM, 1024)
+                                               : sdesc_sw128(sA + ks * 32, 16, 1024);
+            const uint64_t bd = FK<KIND>::B_MN ? sdesc_sw128(sB + ks * 2048, ATOM, 1024)
+                                               : sdesc_sw128(sB + ks * 32, 16, 1024);
+            umma_bf16_pair(d_tmem, ad, bd, IDESC, kb > w.kb0 || ks > 0);
+          }
+          umma_commit_pair(&empty_bar[stage]);
+          if (++stage == PSTAGES) { stage = 0; phase ^= 1; }
+        }
+        umma_commit_pair(&tfull_bar[acc]);
+      }
+    mma_done:;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;                      // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;            // which half of the tile's columns
+    const int rloc = rank * BM + q * 32 + lane;  // row of the tile owned by this thread
+    const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
+    uint8_t* otile = smem + PSTAGES * PSTAGE + (warp - 2) * 4096;
+    int obuf = 0;
+    int it = 0;
+    // what the epilogue reads of memory (H; the addend) is loaded ahead in
+    // 32-column chunks, across tiles: PRE chunks before they are needed
+    constexpr int CH = (KIND == F_UP ? PN / 4 : PN / 2) / 32;   // chunks of a tile per warp
+    constexpr int PRE = KIND == F_DAP ? 1 : 2;
+    constexpr bool RD1 = KIND == F_DAP || KIND == F_DOWN || KIND == F_DX;
+    uint4 n1[RD1 ? PRE : 1][4], n3[KIND == F_DAP ? PRE : 1][4];
+    const bool rd = KIND == F_DAP || (RD1 && a.addend != nullptr);
+    auto fetch = [&](int u, int j, int slot) {   // chunk j of unit u
+      if (u >= units) return;
+      const FTile ti = f_tile<KIND, PN, 2 * BM>(f_unit(u, a).tile, a);
+      const int row = ti.m0 + rloc, col = ti.n0 + (half * CH + j) * 32;
+      const bool live = row < a.M[0];
+      if constexpr (KIND == F_DAP) {
+        const __nv_bfloat16* rp = a.hin + (size_t)row * 2 * a.f;
+        ld_row32(rp, col, a.N[0], live, n1[slot]);
+        ld_row32(rp + a.f, col, a.N[0], live, n3[slot]);
+      } else if constexpr (RD1) {
+        ld_row32(a.addend + (size_t)row * a.N[0], col, a.N[0], live, n1[slot]);
+      }
+    };
+    if (rd) {
+#pragma unroll
+      for (int j = 0; j < PRE; ++j) fetch(pair, j, j);
+    }
+    // Every epilogue warp walks every unit, also after a wait expired (the
+    // waits then return at once): the barriers of split tiles need all of them.
+    for (int u = pair; u < units; u += npairs, ++it) {
+      const FUnit w = f_unit(u, a);
+      const FTile ti = f_tile<KIND, PN, 2 * BM>(w.tile, a);
+      const int acc = it & 1;
+      const int row0 = ti.m0 + rank * BM + q * 32;
+      const int M = a.M[ti.p], N = a.N[ti.p];
+      bounded_wait(&tfull_bar[acc], (it >> 1) & 1, &s_abort, a.status, 4, a.wait_ns);
+      fence_after_sync();
+      const uint32_t tbase = tlane + acc * PN;
+      float v[32];
+      uint32_t r[32];
+      const float4* others = nullptr;   // this warp's rows of part 0
+      int mine = 0;
+      bool finish = true;
+      if (w.slot >= 0) {
+        mine = w.slot % a.parts;
+        float4* pb = a.part + ((size_t)w.slot * 2 + rank) * PART4 + (q * 8) * 8 * 32 + lane;
+        others = pb - (ptrdiff_t)mine * 2 * PART4;
+#pragma unroll 1
+        for (int c = half * 4; c < half * 4 + 4; ++c) {
+          tmem_ld32(tbase + c * 32, r);
+          tmem_ld_wait();
+          if (row0 < M) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              __stcg(pb + (c * 8 + i) * 32,
+                     make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
+          }
+        }
+        __threadfence();
+        epi_barrier();
+        if (threadIdx.x == 64) {
+          s_last = atomicAdd(&a.count[(w.tile - a.whole) * 2 + rank], 1) == a.parts - 1;
+          __threadfence();
+        }
+        epi_barrier();
+        finish = s_last != 0;
+      }
+      // columns 32 cc .. of this thread's row, over all parts in part order
+      auto chunk = [&](int cc, float (&x)[32]) {
+        tmem_ld32(tbase + cc * 32, r);
+        tmem_ld_wait();
+        if (others == nullptr) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+          return;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+#pragma unroll 1
+        for (int p = 0; p < a.parts; ++p) {
+          if (p == mine) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(r[i]);
+          } else if (row0 < M) {
+            const float4* op = others + (size_t)p * 2 * PART4 + cc * 8 * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y = __ldcg(op + i * 32);
+              x[4 * i] += y.x; x[4 * i + 1] += y.y; x[4 * i + 2] += y.z; x[4 * i + 3] += y.w;
+            }
+          }
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int cc = half * CH + j, col = ti.n0 + cc * 32;
+        const bool inside = finish && col < N && row0 < M;   // else nothing of the box is stored
+        if constexpr (KIND == F_UP) {
+          if (!inside) continue;
+          float h3[32];
+          chunk(cc, v);
+          chunk(PN / 64 + cc, h3);
+          if (a.save_h) {
+            stage_store(otile, obuf, v, &a.sO[0], col, row0, lane);
+            stage_store(otile, obuf, h3, &a.sO[1], col, row0, lane);
+          }
+          // A from the accumulator, not from the rounded H: one rounding less
+          // between x and y (2-norm error of y 2.4e-3 instead of 3.1e-3)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * h3[i];
+          stage_store(otile, obuf, v, &a.sO[2], col, row0, lane);
+        } else if constexpr (KIND == F_DAP) {
+          float d3[32];
+          if (inside) {
+            chunk(cc, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float h1 = bf16_lane(n1[j % PRE], i), h3 = bf16_lane(n3[j % PRE], i);
+              const float da = v[i];
+              const float sg = sigmoid_fast(h1);
+              const float sl = h1 * sg;
+              v[i] = da * h3 * (sg * (1.0f + h1 * (1.0f - sg)));
+              d3[i] = da * sl;
+              r[i] = __float_as_uint(sl * h3);
+            }
+          }
+          if (j + PRE < CH) fetch(u, j + PRE, j % PRE);
+          else fetch(u + npairs, j + PRE - CH, j % PRE);
+          if (!inside) continue;
+          stage_store(otile, obuf, v, &a.sO[0], col, row0, lane);
+          stage_store(otile, obuf, d3, &a.sO[1], col, row0, lane);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          stage_store(otile, obuf, v, &a.sO[2], col, row0, lane);
+        } else {
+          if (inside) chunk(cc, v);
+          if constexpr (RD1) {
+            if (rd) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] += bf16_lane(n1[j % PRE], i);
+              if (j + PRE < CH) fetch(u, j + PRE, j % PRE);
+              else fetch(u + npairs, j + PRE - CH, j % PRE);
+            }
+          }
+          if (!inside) continue;
+          stage_store(otile, obuf, v, &a.sO[KIND == F_DW ? ti.p : 0], col, row0, lane);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(smem_u32(&tempty_bar[acc]), 0));
+    }
+  }
+
+  if (warp >= 2 && lane == 0) bulk_wait_all();   // the stores end before the CTA does
+  if (s_abort) {   // aborted: let copies and MMAs in flight land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();              // nothing arrives at a CTA that has left
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ============================================================== launches
+const char* f_name(int kind) {
+  static const char* n[] = {"ffn_up", "ffn_down", "ffn_dap", "ffn_dx", "ffn_dw"};
+  return n[kind];
+}
+
+template <class K>
+int f_go(K kernel, const FfnArgs& a, int kind, int grid, int cluster, int smem, bool dependent,
+         cudaStream_t s) {
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
     return cuda_fail(e, "ffn smem attribute");
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = THREADS;
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at;
-  if (SPLIT) {
-    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    at[cfg.numAttrs].val.clusterDim.x = cluster;
-    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
-    ++cfg.numAttrs;
-  }
-  if (dependent) {
-    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-    ++cfg.numAttrs;
-  }
-  ProfScope _ps(kNames[KIND], s);
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, k_ffn<KIND, BN, SPLIT>, a)) return cuda_fail(e, "ffn");
+  cfg.numAttrs = dependent ? 2 : 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  ProfScope _ps(f_name(kind), s);
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a)) return cuda_fail(e, "ffn");
   return MOE_OK;
 }
 
-// Whole waves of tiles run one tile per CTA.  What is left over (all tiles,
-// when there are few rows) is split along K over clusters of 2, 4 or 8 CTAs,
-// as wide as the SMs hold at once: clusters do not straddle GPCs, so about
-// 128 CTAs in clusters of 8 and 140 in smaller ones are resident.
-int split_width(int rem, int kbs) {
-  for (int c = 8; c >= 2; c /= 2)
-    if (rem * c <= (c == 8 ? 128 : 140) && kbs >= c) return c;
-  return 1;
+// How one product is cut: BN columns and `cluster` CTAs per 128-row tile
+// (k_ffn_split, few tiles), or pairs with the last `tiles - whole` tiles in
+// `parts` (k_ffn_pair).
+struct FPlan {
+  bool split;
+  int bn, cluster;
+  int whole, parts, tiles;
+};
+
+// CTAs of clusters of that size that are resident at once, one per SM
+// (cudaOccupancyMaxActiveClusters: clusters do not straddle the GPCs).
+int resident(int cluster) {
+  static const int n[] = {0, 148, 148, 135, 132, 130, 132, 105, 120};
+  return n[cluster];
 }
 
-template <int KIND, int BN>
-int f_launch_bn(FfnArgs& a, bool dependent, cudaStream_t s) {
+int count_tiles(int kind, int d, int f, int T, int rows, int cols) {
+  auto up = [](int a, int b) { return (a + b - 1) / b; };
+  switch (kind) {
+    case F_UP: return up(T, rows) * up(f, cols / 2);
+    case F_DAP: return up(T, rows) * up(f, cols);
+    case F_DW: return 2 * up(d, rows) * up(f, cols) + up(f, rows) * up(d, cols);
+    default: return up(T, rows) * up(d, cols);
+  }
+}
+
+FPlan f_plan(int kind, int T, int d, int f) {
+  FPlan p = {};
+  const int kd = (d + BK - 1) / BK, kf = (f + BK - 1) / BK, kt = (T + BK - 1) / BK;
+  const int kbs = kind == F_DW ? kt : (kind == F_DX ? 2 * kf : (kind == F_DOWN ? kf : kd));
+  // Few tiles: clusters, if two or more CTAs can share a tile.
+  for (int bn = 256; bn >= 128; bn /= 2) {
+    const int tiles = count_tiles(kind, d, f, T, BM, bn);
+    int c = 8;
+    while (c > 1 && (tiles * c > resident(c) || kbs < c)) --c;
+    const bool fits = tiles <= 148 && (c > 1 || T <= BM);
+    if (fits && (!p.split || tiles * c > count_tiles(kind, d, f, T, BM, p.bn) * p.cluster)) {
+      p.split = true;
+      p.bn = bn;
+      p.cluster = c;
+      p.tiles = tiles;
+    }
+  }
+  if (p.split) return p;
+  p.tiles = count_tiles(kind, d, f, T, 2 * BM, PN);
+  const int rem = p.tiles % MAX_PAIRS;
+  p.parts = rem ? MAX_PAIRS / rem : 1;
+  while (p.parts > 1 && kbs < 2 * p.parts) --p.parts;
+  p.whole = p.parts > 1 ? p.tiles - rem : p.tiles;
+  return p;
+}
+
+template <int KIND>
+int f_launch(FfnArgs& a, bool dependent, cudaStream_t s) {
+  const FPlan p = f_plan(KIND, a.T, a.d, a.f);
   a.status = status_ptr();
   a.wait_ns = WAIT_LIMIT_NS;
   a.dbg_no_load = 0;
@@ -509,28 +773,23 @@ int f_launch_bn(FfnArgs& a, bool dependent, cudaStream_t s) {
     a.wait_ns = (uint64_t)dbg;
     a.dbg_no_load = 1;
   }
-  int tiles = 0;
-  for (int p = 0; p < (KIND == F_DW ? 3 : 1); ++p) {
-    a.mtiles[p] = (a.M[p] + BM - 1) / BM;
-    const int bn = KIND == F_UP ? BN / 2 : BN;
-    a.ntiles[p] = (a.N[p] + bn - 1) / bn;
-    tiles += a.mtiles[p] * a.ntiles[p];
+  const int rows = p.split ? BM : 2 * BM, bn = p.split ? p.bn : PN, cols = KIND == F_UP ? bn / 2 : bn;
+  for (int i = 0; i < (KIND == F_DW ? 3 : 1); ++i) {
+    a.mtiles[i] = (a.M[i] + rows - 1) / rows;
+    a.ntiles[i] = (a.N[i] + cols - 1) / cols;
   }
-  const int sms = device_sm_count();
-  const int rem = tiles % sms, c = rem ? split_width(rem, a.kbs) : 1;
-  const int whole = c > 1 ? tiles - rem : tiles;
-  if (whole > 0) {
-    a.tile0 = 0;
-    a.tiles = whole;
-    if (int rc = f_go<KIND, BN, false>(a, whole < sms ? whole : sms, 1, dependent, s)) return rc;
-    dependent = true;
+  a.tiles = p.tiles;
+  a.whole = p.whole;
+  a.parts = p.parts;
+  if (p.split) {
+    const int grid = p.tiles * p.cluster;
+    return p.bn == 256
+               ? f_go(k_ffn_split<KIND, 256>, a, KIND, grid, p.cluster, FCfg<256>::SMEM, dependent, s)
+               : f_go(k_ffn_split<KIND, 128>, a, KIND, grid, p.cluster, FCfg<128>::SMEM, dependent, s);
   }
-  if (whole < tiles) {
-    a.tile0 = whole;
-    a.tiles = tiles;
-    return f_go<KIND, BN, true>(a, rem * c, c, dependent, s);
-  }
-  return MOE_OK;
+  const int units = p.whole + (p.tiles - p.whole) * p.parts;
+  return f_go(k_ffn_pair<KIND>, a, KIND, 2 * (units < MAX_PAIRS ? units : MAX_PAIRS), 2, PSMEM,
+              dependent, s);
 }
 
 // An MN-major operand [rows, cols]: one box of `atoms` 64-column blocks where
@@ -541,98 +800,157 @@ int map_mn(CUtensorMap* m, const void* p, int cols, int rows, int ld, int atoms,
                   : make_map_2d(m, p, cols, rows, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, ld);
 }
 
-void set_out(FfnArgs& a, int i, void* p, int ld) {
+// Output i: [rows, cols] at p, rows ld elements apart.
+int set_out(FfnArgs& a, int i, void* p, int cols, int rows, int ld) {
   a.out[i] = (__nv_bfloat16*)p;
   a.ldo[i] = ld;
+  return make_map_2d(&a.sO[i], p, cols, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, ld);
 }
 
 }  // namespace
 
-int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, cudaStream_t s) {
+// Partials and counters of the split tiles of a call's products (one region,
+// used by one product after the other); the counters are zeroed first.
+struct FScratch {
+  size_t part_bytes = 0, counts = 0;
+};
+FScratch ffn_scratch(int T, int d, int f, bool bwd) {
+  FScratch z;
+  const int fwd_kinds[] = {F_UP, F_DOWN}, bwd_kinds[] = {F_DAP, F_DX, F_DW};
+  for (int i = 0; i < (bwd ? 3 : 2); ++i) {
+    const FPlan p = f_plan(bwd ? bwd_kinds[i] : fwd_kinds[i], T, d, f);
+    if (p.split || p.parts <= 1) continue;
+    const size_t b = (size_t)(p.tiles - p.whole) * p.parts * 2 * PART4 * sizeof(float4);
+    z.part_bytes = z.part_bytes > b ? z.part_bytes : b;
+    z.counts += (size_t)(p.tiles - p.whole) * 2;
+  }
+  return z;
+}
+size_t ffn_scratch_bytes(int T, int d, int f, bool bwd) {
+  const FScratch z = ffn_scratch(T, d, f, bwd);
+  return z.part_bytes + align_up(z.counts * sizeof(int), 256);
+}
+
+namespace {
+// Hands the scratch out to the products of one call.
+struct FCall {
+  FScratch z;
+  int* count = nullptr;
+  char* base;
+  int T, d, f;
+  cudaStream_t s;
+  bool first = true;
+  FCall(const FfnDense& p, bool bwd, void* scratch, cudaStream_t st)
+      : z(ffn_scratch(p.T, p.d, p.f, bwd)), base((char*)scratch), T(p.T), d(p.d), f(p.f), s(st) {}
+  int begin() {
+    count = (int*)(base + z.part_bytes);
+    if (z.counts)
+      if (cudaError_t e = cudaMemsetAsync(count, 0, z.counts * sizeof(int), s))
+        return cuda_fail(e, "ffn counters");
+    return MOE_OK;
+  }
+  FfnArgs args() const {
+    FfnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.T = T;
+    a.d = d;
+    a.f = f;
+    return a;
+  }
+  template <int KIND>
+  int go(FfnArgs& a) {
+    const FPlan p = f_plan(KIND, T, d, f);
+    a.part = (float4*)base;
+    a.count = count;
+    if (!p.split && p.parts > 1) count += (p.tiles - p.whole) * 2;
+    const bool dependent = !first;
+    first = false;
+    return f_launch<KIND>(a, dependent, s);
+  }
+};
+
+// Columns of B that one CTA loads per stage.
+template <int KIND>
+int b_cols(int T, int d, int f) {
+  const FPlan p = f_plan(KIND, T, d, f);
+  const int n = p.split ? p.bn : PN / 2;
+  return KIND == F_UP && p.split ? n / 2 : n;
+}
+}  // namespace
+
+int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, void* scratch,
+            cudaStream_t s) {
   const int T = p.T, d = p.d, f = p.f;
   int rc;
   bool b4;
+  FCall call(p, false, scratch, s);
+  if ((rc = call.begin())) return rc;
   {  // UP
-    FfnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.T = T; a.d = d; a.f = f;
+    FfnArgs a = call.args();
     a.M[0] = T; a.N[0] = f;
     a.kbs = (d + BK - 1) / BK;
     a.save_h = H != nullptr;
-    const __nv_bfloat16* h = (const __nv_bfloat16*)H;
+    __nv_bfloat16* h = (__nv_bfloat16*)H;
+    const int atoms = b_cols<F_UP>(T, d, f) / 64;
     if ((rc = make_map_2d(&a.mA[0], p.x, d, T, 64, BM))) return rc;
-    if ((rc = map_mn(&a.mB[0], p.w1, f, d, f, 256 / 128, &b4))) return rc;
-    if ((rc = map_mn(&a.mB[1], p.w3, f, d, f, 256 / 128, &b4))) return rc;
+    if ((rc = map_mn(&a.mB[0], p.w1, f, d, f, atoms, &b4))) return rc;
+    if ((rc = map_mn(&a.mB[1], p.w3, f, d, f, atoms, &b4))) return rc;
     a.b4 = b4;
     if (H) {
-      if ((rc = make_map_2d(&a.sO[0], h, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
-      if ((rc = make_map_2d(&a.sO[1], h + f, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
+      if ((rc = set_out(a, 0, h, f, T, 2 * f))) return rc;
+      if ((rc = set_out(a, 1, h + f, f, T, 2 * f))) return rc;
     }
-    if ((rc = make_store_map(&a.sO[2], act, f, T))) return rc;
-    set_out(a, 0, (void*)h, 2 * f);
-    set_out(a, 1, (void*)(h + f), 2 * f);
-    set_out(a, 2, act, f);
-    if ((rc = f_launch_bn<F_UP, 256>(a, false, s))) return rc;
+    if ((rc = set_out(a, 2, act, f, T, f))) return rc;
+    if ((rc = call.go<F_UP>(a))) return rc;
   }
   {  // DOWN
-    FfnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.T = T; a.d = d; a.f = f;
+    FfnArgs a = call.args();
     a.M[0] = T; a.N[0] = d;
     a.kbs = (f + BK - 1) / BK;
     a.addend = (const __nv_bfloat16*)addend;
     if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, BM))) return rc;
-    if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, 256 / 64, &b4))) return rc;
+    if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, b_cols<F_DOWN>(T, d, f) / 64, &b4))) return rc;
     a.b4 = b4;
-    if ((rc = make_store_map(&a.sO[0], y, d, T))) return rc;
-    set_out(a, 0, y, d);
-    if ((rc = f_launch_bn<F_DOWN, 256>(a, true, s))) return rc;
+    if ((rc = set_out(a, 0, y, d, T, d))) return rc;
+    if ((rc = call.go<F_DOWN>(a))) return rc;
   }
   return MOE_OK;
 }
 
 int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* addend, void* dH,
-            void* act, void* dx, void* dw1, void* dw3, void* dw2, cudaStream_t s) {
+            void* act, void* dx, void* dw1, void* dw3, void* dw2, void* scratch, cudaStream_t s) {
   const int T = p.T, d = p.d, f = p.f;
   __nv_bfloat16* dh = (__nv_bfloat16*)dH;
   int rc;
+  FCall call(p, true, scratch, s);
+  if ((rc = call.begin())) return rc;
   {  // DAP
-    FfnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.T = T; a.d = d; a.f = f;
+    FfnArgs a = call.args();
     a.M[0] = T; a.N[0] = f;
     a.kbs = (d + BK - 1) / BK;
     a.hin = (const __nv_bfloat16*)H;
     if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, BM))) return rc;
-    if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, 256))) return rc;
-    if ((rc = make_map_2d(&a.sO[0], dh, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
-    if ((rc = make_map_2d(&a.sO[1], dh + f, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
-    if ((rc = make_store_map(&a.sO[2], act, f, T))) return rc;
-    set_out(a, 0, dh, 2 * f);
-    set_out(a, 1, dh + f, 2 * f);
-    set_out(a, 2, act, f);
-    if ((rc = f_launch_bn<F_DAP, 256>(a, false, s))) return rc;
+    if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, b_cols<F_DAP>(T, d, f)))) return rc;
+    if ((rc = set_out(a, 0, dh, f, T, 2 * f))) return rc;
+    if ((rc = set_out(a, 1, dh + f, f, T, 2 * f))) return rc;
+    if ((rc = set_out(a, 2, act, f, T, f))) return rc;
+    if ((rc = call.go<F_DAP>(a))) return rc;
   }
   {  // DX
-    FfnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.T = T; a.d = d; a.f = f;
+    FfnArgs a = call.args();
     a.M[0] = T; a.N[0] = d;
     a.kbh = (f + BK - 1) / BK;
     a.kbs = 2 * a.kbh;
     a.addend = (const __nv_bfloat16*)addend;
     for (int h = 0; h < 2; ++h) {
       if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B, 2 * f))) return rc;
-      if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, 256))) return rc;
+      if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, b_cols<F_DX>(T, d, f)))) return rc;
     }
-    if ((rc = make_store_map(&a.sO[0], dx, d, T))) return rc;
-    set_out(a, 0, dx, d);
-    if ((rc = f_launch_bn<F_DX, 256>(a, true, s))) return rc;
+    if ((rc = set_out(a, 0, dx, d, T, d))) return rc;
+    if ((rc = call.go<F_DX>(a))) return rc;
   }
   {  // DW
-    FfnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.T = T; a.d = d; a.f = f;
+    FfnArgs a = call.args();
     a.kbs = (T + BK - 1) / BK;
     const struct { const void *A, *B; void* o; int M, N, lda, ldb; } w[3] = {
         {p.x, dh, dw1, d, f, d, 2 * f}, {p.x, dh + f, dw3, d, f, d, 2 * f}, {act, dout, dw2, f, d, f, d}};
@@ -641,13 +959,12 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
       a.M[i] = w[i].M;
       a.N[i] = w[i].N;
       if ((rc = map_mn(&a.mA[i], w[i].A, w[i].M, T, w[i].lda, BM / 64, &a4))) return rc;
-      if ((rc = map_mn(&a.mB[i], w[i].B, w[i].N, T, w[i].ldb, 256 / 64, &b4))) return rc;
+      if ((rc = map_mn(&a.mB[i], w[i].B, w[i].N, T, w[i].ldb, b_cols<F_DW>(T, d, f) / 64, &b4))) return rc;
       a.a4 |= (int)a4 << i;
       a.b4 |= (int)b4 << i;
-      if ((rc = make_store_map(&a.sO[i], w[i].o, w[i].N, w[i].M))) return rc;
-      set_out(a, i, w[i].o, w[i].N);
+      if ((rc = set_out(a, i, w[i].o, w[i].N, w[i].M, w[i].N))) return rc;
     }
-    if ((rc = f_launch_bn<F_DW, 256>(a, true, s))) return rc;
+    if ((rc = call.go<F_DW>(a))) return rc;
   }
   return MOE_OK;
 }

@@ -131,11 +131,14 @@ struct FfnDense {
   const void *x, *w1, *w3, *w2;   // [T, d], [d, f], [d, f], [f, d] bf16
   int T, d, f;
 };
-// H [T, 2f] or null; act [T, f] workspace; addend [T, d] or null.
-int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, cudaStream_t s);
+// H [T, 2f] or null; act [T, f] workspace; addend [T, d] or null; scratch:
+// ffn_scratch_bytes() for the split tiles (16-byte aligned).
+size_t ffn_scratch_bytes(int T, int d, int f, bool bwd);
+int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, void* scratch,
+            cudaStream_t s);
 // dH [T, 2f] and act [T, f]: workspace.
 int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* addend, void* dH,
-            void* act, void* dx, void* dw1, void* dw3, void* dw2, cudaStream_t s);
+            void* act, void* dx, void* dw1, void* dw3, void* dw2, void* scratch, cudaStream_t s);
 
 // ---------------------------------------------------------------- layer norm (norm.cu)
 int launch_layernorm_fwd(const void* x, int64_t ldx, const void* w, const void* b, int T, int d,
