@@ -29,14 +29,15 @@ struct FfnArgs {
   CUtensorMap mA[3];   // DX: dH1, dH3; DW: the three products' A
   CUtensorMap mB[3];   // UP: W1, W3; DX: W1, W3; DW: the three products' B
   CUtensorMap sO[3];   // outputs (UP: H1, H3, A; DAP: dH1, dH3, A; DW: dW1, dW3, dW2)
+  CUtensorMap eI[2];   // what the pairs' epilogues read (DAP: H1, H3; DOWN, DX: the addend)
   int T, d, f;
   int M[3], N[3];      // output rows and columns (UP: N counts the W1 columns)
   int mtiles[3], ntiles[3];
   int tiles;           // output tiles
-  int whole, parts;    // pairs: tiles below `whole` are computed by one pair, the
-                       // others by `parts` pairs along K each
-  float4* part;        // pairs: fp32 partials [split tile * parts + p][rank][PART4]
-  int* count;          // pairs: arrivals [split tile][rank], zero at the start
+  int whole, share;    // pairs: tiles below `whole` are one pair's each; the k-blocks
+                       // of the others, end to end, are cut into shares (0: none)
+  float4* part;        // pairs: fp32 partials [pair][first or second segment][rank][PART4]
+  int* count;          // pairs: arrivals [shared tile][rank], zero at the start
   int kbs, kbh;        // k-blocks per tile; DX: of them with dH1
   int a4, b4;          // operand widths are multiples of 64: one box per stage
   int save_h;          // UP: write H
@@ -112,15 +113,6 @@ __device__ __forceinline__ void load_mn_pair(uint8_t* dst, const CUtensorMap* m,
     tma_load_2d_pair(dst, m, bar, c0, k0);
     tma_load_2d_pair(dst + ATOM, m, bar, c0 + 64, k0);
   }
-}
-
-// 32 bf16 at p[col..], zeros at and past `limit` (a multiple of 8) and for dead rows.
-__device__ __forceinline__ void ld_row32(const __nv_bfloat16* p, int col, int limit, bool live,
-                                         uint4 (&q)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = live && col + 8 * i < limit ? *reinterpret_cast<const uint4*>(p + col + 8 * i)
-                                       : make_uint4(0, 0, 0, 0);
 }
 
 // 8 bf16 results to p (16-byte aligned).
@@ -357,49 +349,95 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
 // not deliver in the 512 clocks the MMAs take.  Persistent; the accumulator is
 // double-buffered in TMEM, six 32 KB stages.
 //
-// The tiles of the last partial wave are cut along K into `parts` units: every
-// unit's epilogue leaves its fp32 partial in global memory (L2), and the unit
-// that arrives last (a counter; nobody waits) adds the others' to its own in
-// part order and runs the epilogue, so the result does not depend on who is
-// last.
+// The tiles of the last partial wave are shared: their k-blocks, end to end,
+// are cut into equal shares, one per pair, so that all pairs end together.  A
+// share covers parts of one or two tiles; every part's epilogue leaves its
+// fp32 partial in global memory (L2), and the part that arrives last (a
+// counter; nobody waits) adds the others' to its own in part order and runs
+// the epilogue, so the result does not depend on who is last.
+//
+// What an epilogue reads of memory (H; the addend) comes by TMA into the
+// warp's own ring of 32 x 32 boxes, ahead of the accumulator, and the result
+// replaces it there and leaves by TMA.
 constexpr int PN = 256;                       // tile columns
-constexpr int PSTAGES = 6;
 constexpr int PSTAGE = 2 * A_BYTES;
-constexpr int PSMEM = PSTAGES * PSTAGE + 8 * 2 * 2048;
 constexpr int PART4 = BM * PN / 4;            // float4s of one CTA's partial
 constexpr int MAX_PAIRS = 74;
+constexpr int BOX = 2048;                     // 32 x 32 bf16, 64-byte swizzle
+
+template <int KIND> struct PCfg {
+  // boxes per epilogue warp: DAP two sets of H1 and H3 and two of A; DOWN and
+  // DX a ring of four; UP and DW two to stage stores
+  static constexpr int BOXES = KIND == F_DAP ? 6 : (KIND == F_DOWN || KIND == F_DX ? 4 : 2);
+  static constexpr int STAGES = KIND == F_DAP ? 4 : (KIND == F_DOWN || KIND == F_DX ? 5 : 6);
+  static constexpr int SMEM = STAGES * PSTAGE + 8 * BOXES * BOX;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
 
 __device__ __forceinline__ void epi_barrier() {   // the 8 epilogue warps
   asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
 }
 
-struct FUnit {
-  int tile, kb0, kb1, slot;   // slot: partial index, or -1 for a whole tile
-};
-__device__ __forceinline__ FUnit f_unit(int u, const FfnArgs& a) {
-  FUnit w;
-  if (u < a.whole) {
-    w.tile = u;
-    w.kb0 = 0;
-    w.kb1 = a.kbs;
-    w.slot = -1;
-  } else {
-    const int v = u - a.whole, p = v % a.parts;
-    w.tile = a.whole + v / a.parts;
-    w.kb0 = (int)((int64_t)a.kbs * p / a.parts);
-    w.kb1 = (int)((int64_t)a.kbs * (p + 1) / a.parts);
-    w.slot = v;
-  }
-  return w;
+// Row `lane` of a box: 16-byte chunk c at chunk c ^ ((lane >> 1) & 3).
+__device__ __forceinline__ void box_get(const uint8_t* box, int lane, uint4 (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = *reinterpret_cast<const uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
 }
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, const float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+    uint4 u;
+    memcpy(&u, h, 16);
+    *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = u;
+  }
+}
+
+// The walk of one pair over its work: whole tiles, then its share.
+struct FWalk {
+  int u, step, lim;      // next whole tile
+  int pos, end;          // k-blocks left of the share
+  int tile, kb0, kb1;    // the current unit
+  int seg;               // shared: 0 or 1, whole: -1
+  __device__ __forceinline__ FWalk(const FfnArgs& a, int pair, int npairs) {
+    u = pair;
+    step = npairs;
+    lim = a.whole;
+    pos = pair * a.share;
+    end = min(pos + a.share, (a.tiles - a.whole) * a.kbs);
+    seg = -1;
+  }
+  __device__ __forceinline__ bool next(const FfnArgs& a) {
+    if (u < lim) {
+      tile = u;
+      u += step;
+      kb0 = 0;
+      kb1 = a.kbs;
+      return true;
+    }
+    if (pos >= end) return false;
+    const int t = pos / a.kbs;
+    tile = a.whole + t;
+    kb0 = pos - t * a.kbs;
+    kb1 = min(a.kbs, end - t * a.kbs);
+    pos = t * a.kbs + kb1;
+    ++seg;
+    return true;
+  }
+};
 
 template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__ FfnArgs a) {
+  using C = PCfg<KIND>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full_bar[PSTAGES];    // used in the even CTA: both CTAs' bytes
-  __shared__ __align__(8) uint64_t empty_bar[PSTAGES];
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];    // used in the even CTA: both CTAs' bytes
+  __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];        // used in the even CTA: both CTAs' warps
+  __shared__ __align__(8) uint64_t box_bar[8][4];        // per epilogue warp: a loaded box (set)
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ volatile int s_abort;
@@ -413,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
   }
   if (threadIdx.x == 0) {
     s_abort = 0;
-    for (int s = 0; s < PSTAGES; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -421,6 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       mbar_init(&tfull_bar[s], 1);
       mbar_init(&tempty_bar[s], 2 * (EPI_THREADS / 32));
     }
+    for (int i = 0; i < 32; ++i) mbar_init(&box_bar[i >> 2][i & 3], 1);
     fence_mbar_init();
     prefetch_tmap(&a.mA[0]);
     prefetch_tmap(&a.mB[0]);
@@ -436,16 +475,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
   const uint32_t tmem_base = s_tmem;
   grid_dependency_wait();      // the previous product's results
   grid_launch_dependents();
-  const int units = a.whole + (a.tiles - a.whole) * a.parts;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     if (lane == 0 && !a.dbg_no_load) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int u = pair; u < units; u += npairs) {
-        const FUnit w = f_unit(u, a);
-        FTile ti = f_tile<KIND, PN, 2 * BM>(w.tile, a);
+      for (FWalk w(a, pair, npairs); w.next(a);) {
+        const FTile ti = f_tile<KIND, PN, 2 * BM>(w.tile, a);
         const int m0 = ti.m0 + rank * BM;
         const int n0 = KIND == F_UP ? ti.n0 : ti.n0 + rank * (PN / 2);   // UP: W1 here, W3 there
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -469,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
             if constexpr (KIND == F_DAP) tma_load_2d_pair(sB, &a.mB[0], bar, k0, n0);
             else load_mn_pair(sB, &a.mB[KIND == F_UP ? rank : 0], bar, k0, n0, a.b4);
           }
-          if (++stage == PSTAGES) { stage = 0; phase ^= 1; }
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
       }
     producer_done:;
@@ -481,8 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
-      for (int u = pair; u < units; u += npairs, ++it) {
-        const FUnit w = f_unit(u, a);
+      for (FWalk w(a, pair, npairs); w.next(a); ++it) {
         const int acc = it & 1;
         if (!bounded_wait(&tempty_bar[acc], ((it >> 1) & 1) ^ 1, &s_abort, a.status, 2, a.wait_ns)) break;
         fence_after_sync();
@@ -501,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
             umma_bf16_pair(d_tmem, ad, bd, IDESC, kb > w.kb0 || ks > 0);
           }
           umma_commit_pair(&empty_bar[stage]);
-          if (++stage == PSTAGES) { stage = 0; phase ^= 1; }
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
         umma_commit_pair(&tfull_bar[acc]);
       }
@@ -511,39 +547,51 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;                      // TMEM lane quarter of this warp
     const int half = (warp - 2) >> 2;            // which half of the tile's columns
-    const int rloc = rank * BM + q * 32 + lane;  // row of the tile owned by this thread
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-    uint8_t* otile = smem + PSTAGES * PSTAGE + (warp - 2) * 4096;
-    int obuf = 0;
-    int it = 0;
-    // what the epilogue reads of memory (H; the addend) is loaded ahead in
-    // 32-column chunks, across tiles: PRE chunks before they are needed
+    uint8_t* boxes = smem + C::STAGES * PSTAGE + (warp - 2) * (C::BOXES * BOX);
     constexpr int CH = (KIND == F_UP ? PN / 4 : PN / 2) / 32;   // chunks of a tile per warp
-    constexpr int PRE = KIND == F_DAP ? 1 : 2;
-    constexpr bool RD1 = KIND == F_DAP || KIND == F_DOWN || KIND == F_DX;
-    uint4 n1[RD1 ? PRE : 1][4], n3[KIND == F_DAP ? PRE : 1][4];
-    const bool rd = KIND == F_DAP || (RD1 && a.addend != nullptr);
-    auto fetch = [&](int u, int j, int slot) {   // chunk j of unit u
-      if (u >= units) return;
-      const FTile ti = f_tile<KIND, PN, 2 * BM>(f_unit(u, a).tile, a);
-      const int row = ti.m0 + rloc, col = ti.n0 + (half * CH + j) * 32;
-      const bool live = row < a.M[0];
-      if constexpr (KIND == F_DAP) {
-        const __nv_bfloat16* rp = a.hin + (size_t)row * 2 * a.f;
-        ld_row32(rp, col, a.N[0], live, n1[slot]);
-        ld_row32(rp + a.f, col, a.N[0], live, n3[slot]);
-      } else if constexpr (RD1) {
-        ld_row32(a.addend + (size_t)row * a.N[0], col, a.N[0], live, n1[slot]);
-      }
-    };
-    if (rd) {
+    constexpr bool READS = KIND == F_DAP || KIND == F_DOWN || KIND == F_DX;
+    constexpr int SETS = KIND == F_DAP ? 2 : C::BOXES;          // boxes (DAP: sets) of the ring
+    const bool rd = KIND == F_DAP || (READS && a.addend != nullptr);
+    uint64_t* bar = box_bar[warp - 2];
+    int obuf = 0, it = 0, g = 0;        // g: chunks so far; chunk g uses set g % SETS
+    // The loads run ahead of the accumulator on a walk of their own.
+    FWalk wl(a, pair, npairs);
+    int lj = CH, lg = 0, lrow = 0, lcol = 0;
+    auto load_next = [&]() {            // lane 0: the next chunk's box (set) into set lg % SETS
+      if (lj == CH) {
+        if (!wl.next(a)) return;
+        const FTile ti = f_tile<KIND, PN, 2 * BM>(wl.tile, a);
+        lrow = ti.m0 + rank * BM + q * 32;
+        lcol = ti.n0 + half * CH * 32;
+        lj = 0;
+        if constexpr (KIND == F_DAP) {
+          // two sets do not cover HBM's latency: the tile's boxes come to L2 first
 #pragma unroll
-      for (int j = 0; j < PRE; ++j) fetch(pair, j, j);
-    }
+          for (int i = 1; i < CH; ++i)
+            if (lrow < a.M[0] && lcol + i * 32 < a.N[0]) {
+              tma_prefetch_2d(&a.eI[0], lcol + i * 32, lrow);
+              tma_prefetch_2d(&a.eI[1], lcol + i * 32, lrow);
+            }
+        }
+      }
+      const int set = lg % SETS;
+      if constexpr (KIND == F_DAP) {
+        mbar_arrive_expect_tx(&bar[set], 2 * BOX);
+        tma_load_2d(boxes + set * 2 * BOX, &a.eI[0], &bar[set], lcol + lj * 32, lrow);
+        tma_load_2d(boxes + set * 2 * BOX + BOX, &a.eI[1], &bar[set], lcol + lj * 32, lrow);
+      } else {
+        mbar_arrive_expect_tx(&bar[set], BOX);
+        tma_load_2d(boxes + set * BOX, &a.eI[0], &bar[set], lcol + lj * 32, lrow);
+      }
+      ++lj;
+      ++lg;
+    };
+    if (rd && lane == 0 && !a.dbg_no_load)
+      for (int i = 0; i < SETS - 1; ++i) load_next();
     // Every epilogue warp walks every unit, also after a wait expired (the
-    // waits then return at once): the barriers of split tiles need all of them.
-    for (int u = pair; u < units; u += npairs, ++it) {
-      const FUnit w = f_unit(u, a);
+    // waits then return at once): the barriers of shared tiles need all of them.
+    for (FWalk w(a, pair, npairs); w.next(a); ++it) {
       const FTile ti = f_tile<KIND, PN, 2 * BM>(w.tile, a);
       const int acc = it & 1;
       const int row0 = ti.m0 + rank * BM + q * 32;
@@ -553,39 +601,45 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       const uint32_t tbase = tlane + acc * PN;
       float v[32];
       uint32_t r[32];
-      const float4* others = nullptr;   // this warp's rows of part 0
-      int mine = 0;
+      int first = 0, parts = 0;     // shared: the tile's first pair and number of parts
       bool finish = true;
-      if (w.slot >= 0) {
-        mine = w.slot % a.parts;
-        float4* pb = a.part + ((size_t)w.slot * 2 + rank) * PART4 + (q * 8) * 8 * 32 + lane;
-        others = pb - (ptrdiff_t)mine * 2 * PART4;
+      const int toff = (w.tile - a.whole) * a.kbs;
+      auto partial = [&](int pr) {  // this warp's corner of pair pr's partial of the tile
+        const int sg = pr * a.share < toff ? 1 : 0;   // its share began in an earlier tile
+        return a.part + (((size_t)pr * 2 + sg) * 2 + rank) * PART4 + (q * 8) * 8 * 32 + lane;
+      };
+      if (w.seg >= 0) {
+        first = toff / a.share;
+        parts = (toff + a.kbs - 1) / a.share - first + 1;
+        float4* pb = partial(pair);
+        if (parts > 1) {
 #pragma unroll 1
-        for (int c = half * 4; c < half * 4 + 4; ++c) {
-          tmem_ld32(tbase + c * 32, r);
-          tmem_ld_wait();
-          if (row0 < M) {
+          for (int c = half * 4; c < half * 4 + 4; ++c) {
+            tmem_ld32(tbase + c * 32, r);
+            tmem_ld_wait();
+            if (row0 < M) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              __stcg(pb + (c * 8 + i) * 32,
-                     make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
+              for (int i = 0; i < 8; ++i)
+                __stcg(pb + (c * 8 + i) * 32,
+                       make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                   __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
+            }
           }
-        }
-        __threadfence();
-        epi_barrier();
-        if (threadIdx.x == 64) {
-          s_last = atomicAdd(&a.count[(w.tile - a.whole) * 2 + rank], 1) == a.parts - 1;
           __threadfence();
+          epi_barrier();
+          if (threadIdx.x == 64) {
+            s_last = atomicAdd(&a.count[(w.tile - a.whole) * 2 + rank], 1) == parts - 1;
+            __threadfence();
+          }
+          epi_barrier();
+          finish = s_last != 0;
         }
-        epi_barrier();
-        finish = s_last != 0;
       }
       // columns 32 cc .. of this thread's row, over all parts in part order
       auto chunk = [&](int cc, float (&x)[32]) {
         tmem_ld32(tbase + cc * 32, r);
         tmem_ld_wait();
-        if (others == nullptr) {
+        if (parts <= 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
           return;
@@ -593,12 +647,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = 0.f;
 #pragma unroll 1
-        for (int p = 0; p < a.parts; ++p) {
-          if (p == mine) {
+        for (int p = 0; p < parts; ++p) {
+          if (first + p == pair) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(r[i]);
           } else if (row0 < M) {
-            const float4* op = others + (size_t)p * 2 * PART4 + cc * 8 * 32;
+            const float4* op = partial(first + p) + cc * 8 * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 y = __ldcg(op + i * 32);
@@ -607,8 +661,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
           }
         }
       };
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
+#pragma unroll 1
+      for (int j = 0; j < CH; ++j, ++g) {
         const int cc = half * CH + j, col = ti.n0 + cc * 32;
         const bool inside = finish && col < N && row0 < M;   // else nothing of the box is stored
         if constexpr (KIND == F_UP) {
@@ -617,21 +671,36 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
           chunk(cc, v);
           chunk(PN / 64 + cc, h3);
           if (a.save_h) {
-            stage_store(otile, obuf, v, &a.sO[0], col, row0, lane);
-            stage_store(otile, obuf, h3, &a.sO[1], col, row0, lane);
+            stage_store(boxes, obuf, v, &a.sO[0], col, row0, lane);
+            stage_store(boxes, obuf, h3, &a.sO[1], col, row0, lane);
           }
           // A from the accumulator, not from the rounded H: one rounding less
           // between x and y (2-norm error of y 2.4e-3 instead of 3.1e-3)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * h3[i];
-          stage_store(otile, obuf, v, &a.sO[2], col, row0, lane);
+          stage_store(boxes, obuf, v, &a.sO[2], col, row0, lane);
+        } else if constexpr (KIND == F_DW) {
+          if (!inside) continue;
+          chunk(cc, v);
+          stage_store(boxes, obuf, v, &a.sO[ti.p], col, row0, lane);
         } else if constexpr (KIND == F_DAP) {
-          float d3[32];
+          const int set = g % SETS;
+          uint8_t* hb = boxes + set * 2 * BOX;
+          // the next chunk's H into the other set, whose results have left it
+          if (lane == 0) {
+            bulk_wait_read<1>();
+            if (!a.dbg_no_load) load_next();
+          }
+          bounded_wait(&bar[set], (g / SETS) & 1, &s_abort, a.status, 5, a.wait_ns);
           if (inside) {
+            uint4 p1[4], p3[4];
+            box_get(hb, lane, p1);
+            box_get(hb + BOX, lane, p3);
             chunk(cc, v);
+            float d3[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float h1 = bf16_lane(n1[j % PRE], i), h3 = bf16_lane(n3[j % PRE], i);
+              const float h1 = bf16_lane(p1, i), h3 = bf16_lane(p3, i);
               const float da = v[i];
               const float sg = sigmoid_fast(h1);
               const float sl = h1 * sg;
@@ -639,27 +708,64 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
               d3[i] = da * sl;
               r[i] = __float_as_uint(sl * h3);
             }
+            __syncwarp();
+            box_put(hb, lane, v);
+            box_put(hb + BOX, lane, d3);
+            fence_proxy_async_smem();
           }
-          if (j + PRE < CH) fetch(u, j + PRE, j % PRE);
-          else fetch(u + npairs, j + PRE - CH, j % PRE);
-          if (!inside) continue;
-          stage_store(otile, obuf, v, &a.sO[0], col, row0, lane);
-          stage_store(otile, obuf, d3, &a.sO[1], col, row0, lane);
+          __syncwarp();
+          if (lane == 0) {
+            if (inside) {
+              tma_store_2d(&a.sO[0], hb, col, row0);
+              tma_store_2d(&a.sO[1], hb + BOX, col, row0);
+            }
+            bulk_commit();
+            bulk_wait_read<2>();   // the A box of two chunks ago has been read
+          }
+          __syncwarp();
+          uint8_t* ab = boxes + (4 + set) * BOX;
+          if (inside) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          stage_store(otile, obuf, v, &a.sO[2], col, row0, lane);
-        } else {
-          if (inside) chunk(cc, v);
-          if constexpr (RD1) {
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            box_put(ab, lane, v);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (inside) tma_store_2d(&a.sO[2], ab, col, row0);
+            bulk_commit();
+          }
+        } else {   // DOWN, DX
+          const int set = g % SETS;
+          uint8_t* box = boxes + set * BOX;
+          if (rd) {
+            bounded_wait(&bar[set], (g / SETS) & 1, &s_abort, a.status, 5, a.wait_ns);
+          } else {
+            if (lane == 0) bulk_wait_read<SETS - 1>();
+            __syncwarp();
+          }
+          if (inside) {
+            uint4 p1[4];
+            if (rd) box_get(box, lane, p1);
+            chunk(cc, v);
             if (rd) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += bf16_lane(n1[j % PRE], i);
-              if (j + PRE < CH) fetch(u, j + PRE, j % PRE);
-              else fetch(u + npairs, j + PRE - CH, j % PRE);
+              for (int i = 0; i < 32; ++i) v[i] += bf16_lane(p1, i);
+            }
+            __syncwarp();
+            box_put(box, lane, v);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (inside) tma_store_2d(&a.sO[0], box, col, row0);
+            bulk_commit();
+            if (rd) {
+              bulk_wait_read<1>();   // the box before this one has been read: refill it
+              if (!a.dbg_no_load) load_next();
             }
           }
-          if (!inside) continue;
-          stage_store(otile, obuf, v, &a.sO[KIND == F_DW ? ti.p : 0], col, row0, lane);
+          __syncwarp();
         }
       }
       fence_before_sync();
@@ -712,12 +818,12 @@ int f_go(K kernel, const FfnArgs& a, int kind, int grid, int cluster, int smem, 
 }
 
 // How one product is cut: BN columns and `cluster` CTAs per 128-row tile
-// (k_ffn_split, few tiles), or pairs with the last `tiles - whole` tiles in
-// `parts` (k_ffn_pair).
+// (k_ffn_split, few tiles), or pairs that share the last `tiles - whole`
+// tiles in shares of `share` k-blocks (k_ffn_pair).
 struct FPlan {
   bool split;
   int bn, cluster;
-  int whole, parts, tiles;
+  int whole, share, tiles;
 };
 
 // CTAs of clusters of that size that are resident at once, one per SM
@@ -741,25 +847,40 @@ FPlan f_plan(int kind, int T, int d, int f) {
   FPlan p = {};
   const int kd = (d + BK - 1) / BK, kf = (f + BK - 1) / BK, kt = (T + BK - 1) / BK;
   const int kbs = kind == F_DW ? kt : (kind == F_DX ? 2 * kf : (kind == F_DOWN ? kf : kd));
-  // Few tiles: clusters, if two or more CTAs can share a tile.
+  // Clocks, for comparison only.  A pair's k-block takes 700 (measured at
+  // 8192 x 7168 x 2048; 512 of MMAs), a split CTA's what 64 bytes per clock
+  // bring in.  Whole waves of pairs; the rest shared where that ends the wave
+  // earlier: a part's partial costs its way through L2, and shares under 12
+  // k-blocks have measured no gain.
+  p.tiles = count_tiles(kind, d, f, T, 2 * BM, PN);
+  const int rem = p.tiles % MAX_PAIRS;
+  const int share = (rem * kbs + MAX_PAIRS - 1) / MAX_PAIRS;
+  p.whole = p.tiles;
+  int64_t best = (int64_t)((p.tiles + MAX_PAIRS - 1) / MAX_PAIRS) * kbs * 700;
+  if (share >= 12) {
+    const int64_t t = (int64_t)(p.tiles / MAX_PAIRS) * kbs * 700 + share * 700 + 6000;
+    if (t < best) {
+      best = t;
+      p.whole -= rem;
+      p.share = share;
+    }
+  }
+  // Few tiles: clusters of at most 8 along K, all resident at once.
   for (int bn = 256; bn >= 128; bn /= 2) {
     const int tiles = count_tiles(kind, d, f, T, BM, bn);
+    if (tiles > 148) continue;
     int c = 8;
     while (c > 1 && (tiles * c > resident(c) || kbs < c)) --c;
-    const bool fits = tiles <= 148 && (c > 1 || T <= BM);
-    if (fits && (!p.split || tiles * c > count_tiles(kind, d, f, T, BM, p.bn) * p.cluster)) {
+    const int64_t t = (int64_t)((kbs + c - 1) / c) * (256 + 2 * bn);
+    if (t < best) {
+      best = t;
       p.split = true;
       p.bn = bn;
       p.cluster = c;
       p.tiles = tiles;
+      p.whole = p.share = 0;
     }
   }
-  if (p.split) return p;
-  p.tiles = count_tiles(kind, d, f, T, 2 * BM, PN);
-  const int rem = p.tiles % MAX_PAIRS;
-  p.parts = rem ? MAX_PAIRS / rem : 1;
-  while (p.parts > 1 && kbs < 2 * p.parts) --p.parts;
-  p.whole = p.parts > 1 ? p.tiles - rem : p.tiles;
   return p;
 }
 
@@ -780,16 +901,15 @@ int f_launch(FfnArgs& a, bool dependent, cudaStream_t s) {
   }
   a.tiles = p.tiles;
   a.whole = p.whole;
-  a.parts = p.parts;
+  a.share = p.share;
   if (p.split) {
     const int grid = p.tiles * p.cluster;
     return p.bn == 256
                ? f_go(k_ffn_split<KIND, 256>, a, KIND, grid, p.cluster, FCfg<256>::SMEM, dependent, s)
                : f_go(k_ffn_split<KIND, 128>, a, KIND, grid, p.cluster, FCfg<128>::SMEM, dependent, s);
   }
-  const int units = p.whole + (p.tiles - p.whole) * p.parts;
-  return f_go(k_ffn_pair<KIND>, a, KIND, 2 * (units < MAX_PAIRS ? units : MAX_PAIRS), 2, PSMEM,
-              dependent, s);
+  const int pairs = p.share || p.whole > MAX_PAIRS ? MAX_PAIRS : p.whole;
+  return f_go(k_ffn_pair<KIND>, a, KIND, 2 * pairs, 2, PCfg<KIND>::SMEM, dependent, s);
 }
 
 // An MN-major operand [rows, cols]: one box of `atoms` 64-column blocks where
@@ -819,9 +939,8 @@ FScratch ffn_scratch(int T, int d, int f, bool bwd) {
   const int fwd_kinds[] = {F_UP, F_DOWN}, bwd_kinds[] = {F_DAP, F_DX, F_DW};
   for (int i = 0; i < (bwd ? 3 : 2); ++i) {
     const FPlan p = f_plan(bwd ? bwd_kinds[i] : fwd_kinds[i], T, d, f);
-    if (p.split || p.parts <= 1) continue;
-    const size_t b = (size_t)(p.tiles - p.whole) * p.parts * 2 * PART4 * sizeof(float4);
-    z.part_bytes = z.part_bytes > b ? z.part_bytes : b;
+    if (p.split || p.share == 0) continue;
+    z.part_bytes = (size_t)MAX_PAIRS * 2 * 2 * PART4 * sizeof(float4);
     z.counts += (size_t)(p.tiles - p.whole) * 2;
   }
   return z;
@@ -862,7 +981,7 @@ struct FCall {
     const FPlan p = f_plan(KIND, T, d, f);
     a.part = (float4*)base;
     a.count = count;
-    if (!p.split && p.parts > 1) count += (p.tiles - p.whole) * 2;
+    if (p.share) count += (p.tiles - p.whole) * 2;
     const bool dependent = !first;
     first = false;
     return f_launch<KIND>(a, dependent, s);
@@ -908,6 +1027,8 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     a.M[0] = T; a.N[0] = d;
     a.kbs = (f + BK - 1) / BK;
     a.addend = (const __nv_bfloat16*)addend;
+    if (addend)
+      if ((rc = make_store_map(&a.eI[0], addend, d, T))) return rc;
     if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, BM))) return rc;
     if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, b_cols<F_DOWN>(T, d, f) / 64, &b4))) return rc;
     a.b4 = b4;
@@ -929,6 +1050,8 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.M[0] = T; a.N[0] = f;
     a.kbs = (d + BK - 1) / BK;
     a.hin = (const __nv_bfloat16*)H;
+    if ((rc = make_map_2d(&a.eI[0], a.hin, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
+    if ((rc = make_map_2d(&a.eI[1], a.hin + f, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
     if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, BM))) return rc;
     if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, b_cols<F_DAP>(T, d, f)))) return rc;
     if ((rc = set_out(a, 0, dh, f, T, 2 * f))) return rc;
@@ -942,6 +1065,8 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.kbh = (f + BK - 1) / BK;
     a.kbs = 2 * a.kbh;
     a.addend = (const __nv_bfloat16*)addend;
+    if (addend)
+      if ((rc = make_store_map(&a.eI[0], addend, d, T))) return rc;
     for (int h = 0; h < 2; ++h) {
       if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B, 2 * f))) return rc;
       if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, b_cols<F_DX>(T, d, f)))) return rc;

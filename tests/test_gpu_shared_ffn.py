@@ -82,6 +82,28 @@ def test_exact(T, d, f, add):
     assert H2 is None and torch.equal(y2, y)
 
 
+@pytest.mark.parametrize("T,d,f", [(10000, 2048, 640), (3000, 1024, 2048), (5000, 2048, 512), (8000, 512, 512),
+                                   (4321, 1992, 1352), (19000, 256, 136)])
+def test_exact_many_rows(T, d, f):
+    """The sizes that CTA pairs compute, with shared last tiles in every product."""
+    c = exact_case(T, d, f, T + d + f)
+    y, H = B.moe_shared_ffn_fwd(c["x"], c["w1"], c["w3"], c["w2"], addend=c["add"])
+    g = B.moe_shared_ffn_bwd(c["dout"], c["x"], c["w1"], c["w3"], c["w2"], H, addend=c["add"])
+    B.moe_check_status()
+    x, w1, w3, w2, do, add = (c[n].double() for n in ("x", "w1", "w3", "w2", "dout", "add"))
+    h1, h3 = x @ w1, x @ w3                       # h1 = 32: silu 32, its slope 1
+    da = do @ w2.T
+    d1, d3, A = da * h3, da * 32, 32 * h3
+    assert d1.abs().max() <= 256                  # dH is exact in bf16
+    ref = dict(y=A @ w2 + add, dx=d1 @ w1.T + d3 @ w3.T + add, dw1=x.T @ d1, dw3=x.T @ d3, dw2=A.T @ do)
+    assert torch.equal(H.double(), torch.cat([h1, h3], 1))
+    for n, got in dict(g, y=y).items():
+        assert ((ref[n].to(BF).double() == ref[n]).double().mean()) > 0.99, n
+        assert torch.equal(got, ref[n].to(BF)), n
+    again = B.moe_shared_ffn_bwd(c["dout"], c["x"], c["w1"], c["w3"], c["w2"], H, addend=c["add"])
+    assert all(torch.equal(again[n], g[n]) for n in g)
+
+
 def random_case(T, d, f, seed, scale=1.0):
     g = torch.Generator().manual_seed(seed)
     n = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(BF).cuda()  # noqa: E731
