@@ -28,14 +28,14 @@ enum FKind : int { F_UP = 0, F_DOWN = 1, F_DAP = 2, F_DX = 3, F_DW = 4 };
 struct FfnArgs {
   CUtensorMap mA[3];   // DX: dH1, dH3; DW: the three products' A
   CUtensorMap mB[3];   // UP: W1, W3; DX: W1, W3; DW: the three products' B
-  CUtensorMap sO[3];   // outputs (UP: H1, H3, A; DAP: dH1, dH3, A; DW: dW1, dW3, dW2)
-  CUtensorMap eI[2];   // what the pairs' epilogues read (DAP: H1, H3; DOWN, DX: the addend)
   int T, d, f;
   int M[3], N[3];      // output rows and columns (UP: N counts the W1 columns)
   int mtiles[3], ntiles[3];
   int tiles;           // output tiles
   int whole, share;    // pairs: tiles below `whole` are one pair's each; the k-blocks
                        // of the others, end to end, are cut into shares (0: none)
+  int span;            // k-blocks a shared tile counts for (>= kbs; a multiple of
+                       // share: its cuts fall at the same k-blocks in every tile)
   float4* part;        // pairs: fp32 partials [pair][first or second segment][rank][PART4]
   int* count;          // pairs: arrivals [shared tile][rank], zero at the start
   int kbs, kbh;        // k-blocks per tile; DX: of them with dH1
@@ -43,8 +43,10 @@ struct FfnArgs {
   int save_h;          // UP: write H
   const __nv_bfloat16* hin;     // DAP
   const __nv_bfloat16* addend;  // DOWN, DX: [T, d] or null
-  // split tiles write their results from registers: rows of o0 / o1 / o2 at
-  // strides ldo, ldo, ldo2 (UP: H1, H3, A; DAP: dH1, dH3, A; DW: per product)
+  CUtensorMap sO[3];   // pairs: the outputs in 32 x 64 boxes
+  CUtensorMap eI[2];   // pairs: what the epilogue reads (DAP: H1, H3; DOWN, DX: the addend)
+  // outputs and their row strides (UP: H1, H3, A; DAP: dH1, dH3, A; DW: dW1,
+  // dW3, dW2; DOWN, DX: one)
   __nv_bfloat16* out[3];
   int ldo[3];
   int* status;
@@ -353,23 +355,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
 // are cut into equal shares, one per pair, so that all pairs end together.  A
 // share covers parts of one or two tiles; every part's epilogue leaves its
 // fp32 partial in global memory (L2), and the part that arrives last (a
-// counter; nobody waits) adds the others' to its own in part order and runs
-// the epilogue, so the result does not depend on who is last.
+// counter; nobody waits) sums them in part order and runs the epilogue, so the
+// result does not depend on who is last.
 //
-// What an epilogue reads of memory (H; the addend) comes by TMA into the
-// warp's own ring of 32 x 32 boxes, ahead of the accumulator, and the result
-// replaces it there and leaves by TMA.
+// Epilogue reads and writes go through boxes of 32 rows x 64 columns in
+// shared memory, one ring per warp, by TMA: what is read (H; the addend)
+// arrives ahead of the accumulator, the result replaces it there and leaves.
+// Boxes of 128-byte rows, since the TMA unit's time goes by rows: with boxes
+// of 32 columns, 64-byte rows, a tile with K = 512 spent longer on its
+// epilogue's boxes than on its main loop (dx at 32768 x 1536 x 256: 69 us),
+// and plain 32-byte accesses from registers took longer still (100 us).
 constexpr int PN = 256;                       // tile columns
 constexpr int PSTAGE = 2 * A_BYTES;
 constexpr int PART4 = BM * PN / 4;            // float4s of one CTA's partial
 constexpr int MAX_PAIRS = 74;
-constexpr int BOX = 2048;                     // 32 x 32 bf16, 64-byte swizzle
+constexpr int BOX = 4096;                     // 32 x 64 bf16, 128-byte swizzle
+constexpr int BOXW = 64;
 
 template <int KIND> struct PCfg {
-  // boxes per epilogue warp: DAP two sets of H1 and H3 and two of A; DOWN and
-  // DX a ring of four; UP and DW two to stage stores
-  static constexpr int BOXES = KIND == F_DAP ? 6 : (KIND == F_DOWN || KIND == F_DX ? 4 : 2);
-  static constexpr int STAGES = KIND == F_DAP ? 4 : (KIND == F_DOWN || KIND == F_DX ? 5 : 6);
+  // boxes per epilogue warp: UP H1, H3 and A of its 64 columns; DAP the same,
+  // read and written in place; DOWN and DX a ring of three; DW two to store
+  static constexpr int BOXES = KIND == F_DW ? 2 : 3;
+  static constexpr int STAGES = KIND == F_DW ? 5 : 4;
   static constexpr int SMEM = STAGES * PSTAGE + 8 * BOXES * BOX;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -378,21 +385,21 @@ __device__ __forceinline__ void epi_barrier() {   // the 8 epilogue warps
   asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
 }
 
-// Row `lane` of a box: 16-byte chunk c at chunk c ^ ((lane >> 1) & 3).
-__device__ __forceinline__ void box_get(const uint8_t* box, int lane, uint4 (&p)[4]) {
+// Columns 32 h .. of row `lane` of a box: 16-byte chunk c at chunk c ^ (lane & 7).
+__device__ __forceinline__ void box_get(const uint8_t* box, int lane, int h, uint4 (&p)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    p[i] = *reinterpret_cast<const uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+    p[i] = *reinterpret_cast<const uint4*>(box + lane * 128 + (((4 * h + i) ^ (lane & 7)) << 4));
 }
-__device__ __forceinline__ void box_put(uint8_t* box, int lane, const float* v) {
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, int h, const float* v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h[4];
+    __nv_bfloat162 b[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+    for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
     uint4 u;
-    memcpy(&u, h, 16);
-    *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = u;
+    memcpy(&u, b, 16);
+    *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + i) ^ (lane & 7)) << 4)) = u;
   }
 }
 
@@ -407,7 +414,7 @@ struct FWalk {
     step = npairs;
     lim = a.whole;
     pos = pair * a.share;
-    end = min(pos + a.share, (a.tiles - a.whole) * a.kbs);
+    end = min(pos + a.share, (a.tiles - a.whole) * a.span);
     seg = -1;
   }
   __device__ __forceinline__ bool next(const FfnArgs& a) {
@@ -419,11 +426,12 @@ struct FWalk {
       return true;
     }
     if (pos >= end) return false;
-    const int t = pos / a.kbs;
+    const int t = pos / a.span;
     tile = a.whole + t;
-    kb0 = pos - t * a.kbs;
-    kb1 = min(a.kbs, end - t * a.kbs);
-    pos = t * a.kbs + kb1;
+    kb0 = pos - t * a.span;
+    kb1 = min(a.span, end - t * a.span);
+    pos = t * a.span + kb1;
+    kb1 = min(kb1, a.kbs);
     ++seg;
     return true;
   }
@@ -437,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];        // used in the even CTA: both CTAs' warps
-  __shared__ __align__(8) uint64_t box_bar[8][4];        // per epilogue warp: a loaded box (set)
+  __shared__ __align__(8) uint64_t box_bar[8][3];        // per epilogue warp: a loaded box
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ volatile int s_abort;
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       mbar_init(&tfull_bar[s], 1);
       mbar_init(&tempty_bar[s], 2 * (EPI_THREADS / 32));
     }
-    for (int i = 0; i < 32; ++i) mbar_init(&box_bar[i >> 2][i & 3], 1);
+    for (int i = 0; i < 24; ++i) mbar_init(&box_bar[i / 3][i % 3], 1);
     fence_mbar_init();
     prefetch_tmap(&a.mA[0]);
     prefetch_tmap(&a.mB[0]);
@@ -549,46 +557,43 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
     const int half = (warp - 2) >> 2;            // which half of the tile's columns
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
     uint8_t* boxes = smem + C::STAGES * PSTAGE + (warp - 2) * (C::BOXES * BOX);
-    constexpr int CH = (KIND == F_UP ? PN / 4 : PN / 2) / 32;   // chunks of a tile per warp
+    constexpr int CH = (KIND == F_UP ? PN / 4 : PN / 2) / BOXW;   // boxes of a tile per warp
     constexpr bool READS = KIND == F_DAP || KIND == F_DOWN || KIND == F_DX;
-    constexpr int SETS = KIND == F_DAP ? 2 : C::BOXES;          // boxes (DAP: sets) of the ring
+    constexpr int SETS = KIND == F_DAP ? 1 : C::BOXES;            // of the ring
     const bool rd = KIND == F_DAP || (READS && a.addend != nullptr);
     uint64_t* bar = box_bar[warp - 2];
-    int obuf = 0, it = 0, g = 0;        // g: chunks so far; chunk g uses set g % SETS
-    // The loads run ahead of the accumulator on a walk of their own.
+    int it = 0, g = 0;                  // g: chunks so far; chunk g uses set g % SETS
+    // The loads run ahead of the accumulator on a walk of their own (lane 0).
     FWalk wl(a, pair, npairs);
     int lj = CH, lg = 0, lrow = 0, lcol = 0;
-    auto load_next = [&]() {            // lane 0: the next chunk's box (set) into set lg % SETS
+    auto load_next = [&]() {            // the next chunk's box(es) into set lg % SETS
       if (lj == CH) {
         if (!wl.next(a)) return;
         const FTile ti = f_tile<KIND, PN, 2 * BM>(wl.tile, a);
         lrow = ti.m0 + rank * BM + q * 32;
-        lcol = ti.n0 + half * CH * 32;
+        lcol = ti.n0 + half * CH * BOXW;
         lj = 0;
-        if constexpr (KIND == F_DAP) {
-          // two sets do not cover HBM's latency: the tile's boxes come to L2 first
+        // the ring does not cover HBM's latency: the next tile's boxes come to L2 now
+        FWalk wn = wl;
+        if (wn.next(a)) {
+          const FTile tn = f_tile<KIND, PN, 2 * BM>(wn.tile, a);
+          const int prow = tn.m0 + rank * BM + q * 32, pcol = tn.n0 + half * CH * BOXW;
 #pragma unroll
-          for (int i = 1; i < CH; ++i)
-            if (lrow < a.M[0] && lcol + i * 32 < a.N[0]) {
-              tma_prefetch_2d(&a.eI[0], lcol + i * 32, lrow);
-              tma_prefetch_2d(&a.eI[1], lcol + i * 32, lrow);
+          for (int i = 0; i < CH; ++i)
+            if (prow < a.M[0] && pcol + i * BOXW < a.N[0]) {
+              tma_prefetch_2d(&a.eI[0], pcol + i * BOXW, prow);
+              if (KIND == F_DAP) tma_prefetch_2d(&a.eI[1], pcol + i * BOXW, prow);
             }
         }
       }
       const int set = lg % SETS;
-      if constexpr (KIND == F_DAP) {
-        mbar_arrive_expect_tx(&bar[set], 2 * BOX);
-        tma_load_2d(boxes + set * 2 * BOX, &a.eI[0], &bar[set], lcol + lj * 32, lrow);
-        tma_load_2d(boxes + set * 2 * BOX + BOX, &a.eI[1], &bar[set], lcol + lj * 32, lrow);
-      } else {
-        mbar_arrive_expect_tx(&bar[set], BOX);
-        tma_load_2d(boxes + set * BOX, &a.eI[0], &bar[set], lcol + lj * 32, lrow);
-      }
+      mbar_arrive_expect_tx(&bar[set], KIND == F_DAP ? 2 * BOX : BOX);
+      tma_load_2d(boxes + set * BOX, &a.eI[0], &bar[set], lcol + lj * BOXW, lrow);
+      if (KIND == F_DAP) tma_load_2d(boxes + BOX, &a.eI[1], &bar[set], lcol + lj * BOXW, lrow);
       ++lj;
       ++lg;
     };
-    if (rd && lane == 0 && !a.dbg_no_load)
-      for (int i = 0; i < SETS - 1; ++i) load_next();
+    if (READS && rd && lane == 0 && !a.dbg_no_load) load_next();
     // Every epilogue warp walks every unit, also after a wait expired (the
     // waits then return at once): the barriers of shared tiles need all of them.
     for (FWalk w(a, pair, npairs); w.next(a); ++it) {
@@ -600,10 +605,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       fence_after_sync();
       const uint32_t tbase = tlane + acc * PN;
       float v[32];
-      uint32_t r[32];
       int first = 0, parts = 0;     // shared: the tile's first pair and number of parts
       bool finish = true;
-      const int toff = (w.tile - a.whole) * a.kbs;
+      const int toff = (w.tile - a.whole) * a.span;
       auto partial = [&](int pr) {  // this warp's corner of pair pr's partial of the tile
         const int sg = pr * a.share < toff ? 1 : 0;   // its share began in an earlier tile
         return a.part + (((size_t)pr * 2 + sg) * 2 + rank) * PART4 + (q * 8) * 8 * 32 + lane;
@@ -611,10 +615,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       if (w.seg >= 0) {
         first = toff / a.share;
         parts = (toff + a.kbs - 1) / a.share - first + 1;
-        float4* pb = partial(pair);
         if (parts > 1) {
+          float4* pb = partial(pair);
 #pragma unroll 1
           for (int c = half * 4; c < half * 4 + 4; ++c) {
+            uint32_t r[32];
             tmem_ld32(tbase + c * 32, r);
             tmem_ld_wait();
             if (row0 < M) {
@@ -637,136 +642,114 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       }
       // columns 32 cc .. of this thread's row, over all parts in part order
       auto chunk = [&](int cc, float (&x)[32]) {
-        tmem_ld32(tbase + cc * 32, r);
-        tmem_ld_wait();
         if (parts <= 1) {
+          uint32_t r[32];
+          tmem_ld32(tbase + cc * 32, r);
+          tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
           return;
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        if (row0 >= M) return;
 #pragma unroll 1
         for (int p = 0; p < parts; ++p) {
-          if (first + p == pair) {
+          const float4* op = partial(first + p) + cc * 8 * 32;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(r[i]);
-          } else if (row0 < M) {
-            const float4* op = partial(first + p) + cc * 8 * 32;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 y = __ldcg(op + i * 32);
-              x[4 * i] += y.x; x[4 * i + 1] += y.y; x[4 * i + 2] += y.z; x[4 * i + 3] += y.w;
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = __ldcg(op + i * 32);
+            x[4 * i] += y.x; x[4 * i + 1] += y.y; x[4 * i + 2] += y.z; x[4 * i + 3] += y.w;
           }
         }
       };
 #pragma unroll 1
       for (int j = 0; j < CH; ++j, ++g) {
-        const int cc = half * CH + j, col = ti.n0 + cc * 32;
+        const int cb = (half * CH + j) * BOXW, col = ti.n0 + cb;
         const bool inside = finish && col < N && row0 < M;   // else nothing of the box is stored
-        if constexpr (KIND == F_UP) {
-          if (!inside) continue;
-          float h3[32];
-          chunk(cc, v);
-          chunk(PN / 64 + cc, h3);
-          if (a.save_h) {
-            stage_store(boxes, obuf, v, &a.sO[0], col, row0, lane);
-            stage_store(boxes, obuf, h3, &a.sO[1], col, row0, lane);
-          }
-          // A from the accumulator, not from the rounded H: one rounding less
-          // between x and y (2-norm error of y 2.4e-3 instead of 3.1e-3)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * h3[i];
-          stage_store(boxes, obuf, v, &a.sO[2], col, row0, lane);
-        } else if constexpr (KIND == F_DW) {
-          if (!inside) continue;
-          chunk(cc, v);
-          stage_store(boxes, obuf, v, &a.sO[ti.p], col, row0, lane);
-        } else if constexpr (KIND == F_DAP) {
-          const int set = g % SETS;
-          uint8_t* hb = boxes + set * 2 * BOX;
-          // the next chunk's H into the other set, whose results have left it
-          if (lane == 0) {
+        const int set = g % SETS;
+        uint8_t* box = boxes + set * BOX;
+        if (READS && rd) {
+          // the next chunk's box into the set whose result left two chunks ago
+          if (KIND != F_DAP && lane == 0) {
             bulk_wait_read<1>();
             if (!a.dbg_no_load) load_next();
           }
           bounded_wait(&bar[set], (g / SETS) & 1, &s_abort, a.status, 5, a.wait_ns);
-          if (inside) {
-            uint4 p1[4], p3[4];
-            box_get(hb, lane, p1);
-            box_get(hb + BOX, lane, p3);
-            chunk(cc, v);
-            float d3[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float h1 = bf16_lane(p1, i), h3 = bf16_lane(p3, i);
-              const float da = v[i];
-              const float sg = sigmoid_fast(h1);
-              const float sl = h1 * sg;
-              v[i] = da * h3 * (sg * (1.0f + h1 * (1.0f - sg)));
-              d3[i] = da * sl;
-              r[i] = __float_as_uint(sl * h3);
-            }
-            __syncwarp();
-            box_put(hb, lane, v);
-            box_put(hb + BOX, lane, d3);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) {
-            if (inside) {
-              tma_store_2d(&a.sO[0], hb, col, row0);
-              tma_store_2d(&a.sO[1], hb + BOX, col, row0);
-            }
-            bulk_commit();
-            bulk_wait_read<2>();   // the A box of two chunks ago has been read
-          }
-          __syncwarp();
-          uint8_t* ab = boxes + (4 + set) * BOX;
-          if (inside) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            box_put(ab, lane, v);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) {
-            if (inside) tma_store_2d(&a.sO[2], ab, col, row0);
-            bulk_commit();
-          }
-        } else {   // DOWN, DX
-          const int set = g % SETS;
-          uint8_t* box = boxes + set * BOX;
-          if (rd) {
-            bounded_wait(&bar[set], (g / SETS) & 1, &s_abort, a.status, 5, a.wait_ns);
-          } else {
-            if (lane == 0) bulk_wait_read<SETS - 1>();
-            __syncwarp();
-          }
-          if (inside) {
-            uint4 p1[4];
-            if (rd) box_get(box, lane, p1);
-            chunk(cc, v);
-            if (rd) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += bf16_lane(p1, i);
-            }
-            __syncwarp();
-            box_put(box, lane, v);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) {
-            if (inside) tma_store_2d(&a.sO[0], box, col, row0);
-            bulk_commit();
-            if (rd) {
-              bulk_wait_read<1>();   // the box before this one has been read: refill it
-              if (!a.dbg_no_load) load_next();
-            }
-          }
+        } else {
+          // the box's (UP: the boxes') last results have left it
+          if (lane == 0) bulk_wait_read<KIND == F_UP ? 0 : SETS - 1>();
           __syncwarp();
         }
+        if (inside) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int cc = cb / 32 + h;
+            if constexpr (KIND == F_UP) {
+              float h3[32];
+              chunk(cc, v);
+              chunk(PN / 64 + cc, h3);
+              if (a.save_h) {
+                box_put(boxes, lane, h, v);
+                box_put(boxes + BOX, lane, h, h3);
+              }
+              // A from the accumulator, not from the rounded H: one rounding less
+              // between x and y (2-norm error of y 2.4e-3 instead of 3.1e-3)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * h3[i];
+              box_put(boxes + 2 * BOX, lane, h, v);
+            } else if constexpr (KIND == F_DAP) {
+              uint4 p1[4], p3[4];
+              box_get(boxes, lane, h, p1);
+              box_get(boxes + BOX, lane, h, p3);
+              chunk(cc, v);
+              float d3[32], av[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float h1 = bf16_lane(p1, i), h3 = bf16_lane(p3, i);
+                const float da = v[i];
+                const float sg = sigmoid_fast(h1);
+                const float sl = h1 * sg;
+                v[i] = da * h3 * (sg * (1.0f + h1 * (1.0f - sg)));
+                d3[i] = da * sl;
+                av[i] = sl * h3;
+              }
+              box_put(boxes, lane, h, v);
+              box_put(boxes + BOX, lane, h, d3);
+              box_put(boxes + 2 * BOX, lane, h, av);
+            } else {
+              uint4 p1[4];
+              if (READS && rd) box_get(box, lane, h, p1);
+              chunk(cc, v);
+              if (READS && rd) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += bf16_lane(p1, i);
+              }
+              box_put(box, lane, h, v);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (inside) {
+            if constexpr (KIND == F_UP || KIND == F_DAP) {
+              if (KIND == F_DAP || a.save_h) {
+                tma_store_2d(&a.sO[0], boxes, col, row0);
+                tma_store_2d(&a.sO[1], boxes + BOX, col, row0);
+              }
+              tma_store_2d(&a.sO[2], boxes + 2 * BOX, col, row0);
+            } else {
+              tma_store_2d(&a.sO[KIND == F_DW ? ti.p : 0], box, col, row0);
+            }
+          }
+          bulk_commit();
+          if (KIND == F_DAP) {   // one set: the next boxes once these have been read
+            bulk_wait_read<0>();
+            if (!a.dbg_no_load) load_next();
+          }
+        }
+        __syncwarp();
       }
       fence_before_sync();
       __syncwarp();
@@ -823,7 +806,7 @@ int f_go(K kernel, const FfnArgs& a, int kind, int grid, int cluster, int smem, 
 struct FPlan {
   bool split;
   int bn, cluster;
-  int whole, share, tiles;
+  int whole, share, span, tiles;
 };
 
 // CTAs of clusters of that size that are resident at once, one per SM
@@ -858,11 +841,22 @@ FPlan f_plan(int kind, int T, int d, int f) {
   p.whole = p.tiles;
   int64_t best = (int64_t)((p.tiles + MAX_PAIRS - 1) / MAX_PAIRS) * kbs * 700;
   if (share >= 12) {
-    const int64_t t = (int64_t)(p.tiles / MAX_PAIRS) * kbs * 700 + share * 700 + 6000;
+    p.span = kbs;
+    p.share = share;
+    // The weight gradients' operands are long and stream from HBM: all tiles
+    // cut at the same k-blocks read them together, which halves the traffic
+    // (32768 x 1536 x 256: 92 us with arbitrary cuts).
+    if (kind == F_DW) {
+      const int parts = MAX_PAIRS / rem;
+      p.share = (kbs + parts - 1) / parts;
+      p.span = (kbs + p.share - 1) / p.share * p.share;
+    }
+    const int64_t t = (int64_t)(p.tiles / MAX_PAIRS) * kbs * 700 + p.share * 700 + 6000;
     if (t < best) {
       best = t;
       p.whole -= rem;
-      p.share = share;
+    } else {
+      p.share = 0;
     }
   }
   // Few tiles: clusters of at most 8 along K, all resident at once.
@@ -902,6 +896,7 @@ int f_launch(FfnArgs& a, bool dependent, cudaStream_t s) {
   a.tiles = p.tiles;
   a.whole = p.whole;
   a.share = p.share;
+  a.span = p.span;
   if (p.split) {
     const int grid = p.tiles * p.cluster;
     return p.bn == 256
@@ -920,11 +915,15 @@ int map_mn(CUtensorMap* m, const void* p, int cols, int rows, int ld, int atoms,
                   : make_map_2d(m, p, cols, rows, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, ld);
 }
 
+// [rows, cols] at p, rows ld elements apart, in the epilogue's boxes.
+int box_map(CUtensorMap* m, const void* p, int cols, int rows, int ld) {
+  return make_map_2d(m, p, cols, rows, BOXW, 32, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+}
 // Output i: [rows, cols] at p, rows ld elements apart.
 int set_out(FfnArgs& a, int i, void* p, int cols, int rows, int ld) {
   a.out[i] = (__nv_bfloat16*)p;
   a.ldo[i] = ld;
-  return make_map_2d(&a.sO[i], p, cols, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, ld);
+  return box_map(&a.sO[i], p, cols, rows, ld);
 }
 
 }  // namespace
@@ -1027,11 +1026,11 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     a.M[0] = T; a.N[0] = d;
     a.kbs = (f + BK - 1) / BK;
     a.addend = (const __nv_bfloat16*)addend;
-    if (addend)
-      if ((rc = make_store_map(&a.eI[0], addend, d, T))) return rc;
     if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, BM))) return rc;
     if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, b_cols<F_DOWN>(T, d, f) / 64, &b4))) return rc;
     a.b4 = b4;
+    if (addend)
+      if ((rc = box_map(&a.eI[0], addend, d, T, d))) return rc;
     if ((rc = set_out(a, 0, y, d, T, d))) return rc;
     if ((rc = call.go<F_DOWN>(a))) return rc;
   }
@@ -1050,10 +1049,10 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.M[0] = T; a.N[0] = f;
     a.kbs = (d + BK - 1) / BK;
     a.hin = (const __nv_bfloat16*)H;
-    if ((rc = make_map_2d(&a.eI[0], a.hin, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
-    if ((rc = make_map_2d(&a.eI[1], a.hin + f, f, T, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, 2 * f))) return rc;
     if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, BM))) return rc;
     if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, b_cols<F_DAP>(T, d, f)))) return rc;
+    if ((rc = box_map(&a.eI[0], a.hin, f, T, 2 * f))) return rc;
+    if ((rc = box_map(&a.eI[1], a.hin + f, f, T, 2 * f))) return rc;
     if ((rc = set_out(a, 0, dh, f, T, 2 * f))) return rc;
     if ((rc = set_out(a, 1, dh + f, f, T, 2 * f))) return rc;
     if ((rc = set_out(a, 2, act, f, T, f))) return rc;
@@ -1065,12 +1064,12 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.kbh = (f + BK - 1) / BK;
     a.kbs = 2 * a.kbh;
     a.addend = (const __nv_bfloat16*)addend;
-    if (addend)
-      if ((rc = make_store_map(&a.eI[0], addend, d, T))) return rc;
     for (int h = 0; h < 2; ++h) {
       if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B, 2 * f))) return rc;
       if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, b_cols<F_DX>(T, d, f)))) return rc;
     }
+    if (addend)
+      if ((rc = box_map(&a.eI[0], addend, d, T, d))) return rc;
     if ((rc = set_out(a, 0, dx, d, T, d))) return rc;
     if ((rc = call.go<F_DX>(a))) return rc;
   }
