@@ -43,8 +43,7 @@ struct FfnArgs {
   int save_h;          // UP: write H
   const __nv_bfloat16* hin;     // DAP
   const __nv_bfloat16* addend;  // DOWN, DX: [T, d] or null
-  CUtensorMap sO[3];   // pairs: the outputs in 32 x 64 boxes
-  CUtensorMap eI[2];   // pairs: what the epilogue reads (DAP: H1, H3; DOWN, DX: the addend)
+  CUtensorMap eO, eI;  // pairs, DOWN and DX: the output and the addend in 32 x 64 boxes
   // outputs and their row strides (UP: H1, H3, A; DAP: dH1, dH3, A; DW: dW1,
   // dW3, dW2; DOWN, DX: one)
   __nv_bfloat16* out[3];
@@ -68,6 +67,27 @@ template <int BN> struct FCfg {
   static_assert(STAGE % 1024 == 0, "stages must keep 1 KB alignment");
   static_assert(BM * BN * 4 <= SMEM && SMEM <= 227 * 1024, "partials reuse the stages");
 };
+
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) from the hardware's approximate 2^x and
+// reciprocal (each within 2^-22; results are rounded to bf16 afterwards).
+// Flushing denormals saves their range handling: about a third of the
+// epilogue's instructions.
+__device__ __forceinline__ float sigmoid_ftz(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
+// SwiGLU backward of one element: from dA and H the two halves of dH, and A.
+__device__ __forceinline__ void swiglu_bwd(float da, float h1, float h3, float& d1, float& d3,
+                                           float& av) {
+  const float sg = sigmoid_ftz(h1);
+  const float sl = h1 * sg;
+  d1 = da * h3 * fmaf(sl, 1.0f - sg, sg);   // silu'(h1) = sg (1 + h1 (1 - sg))
+  d3 = da * sl;
+  av = sl * h3;
+}
 
 struct FTile {
   int p, m0, n0;
@@ -294,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
           st_bf16x8(a.out[1] + row * a.ldo[1] + col, h3);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * sigmoid_fast(v[k]) * h3[k];
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * sigmoid_ftz(v[k]) * h3[k];
         st_bf16x8(a.out[2] + row * a.ldo[2] + col, v);
       } else if constexpr (KIND == F_DAP) {
         uint4 p1[4], p3[4];
@@ -305,12 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
         float d3[8], av[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float h1 = bf16_lane(p1, k), h3 = bf16_lane(p3, k), da = v[k];
-          const float sg = sigmoid_fast(h1);
-          const float sl = h1 * sg;
-          v[k] = da * h3 * (sg * (1.0f + h1 * (1.0f - sg)));
-          d3[k] = da * sl;
-          av[k] = sl * h3;
+          swiglu_bwd(v[k], bf16_lane(p1, k), bf16_lane(p3, k), v[k], d3[k], av[k]);
         }
         st_bf16x8(a.out[0] + row * a.ldo[0] + col, v);
         st_bf16x8(a.out[1] + row * a.ldo[1] + col, d3);
@@ -358,31 +373,88 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
 // counter; nobody waits) sums them in part order and runs the epilogue, so the
 // result does not depend on who is last.
 //
-// Epilogue reads and writes go through boxes of 32 rows x 64 columns in
-// shared memory, one ring per warp, by TMA: what is read (H; the addend)
-// arrives ahead of the accumulator, the result replaces it there and leaves.
-// Boxes of 128-byte rows, since the TMA unit's time goes by rows: with boxes
-// of 32 columns, 64-byte rows, a tile with K = 512 spent longer on its
-// epilogue's boxes than on its main loop (dx at 32768 x 1536 x 256: 69 us),
-// and plain 32-byte accesses from registers took longer still (100 us).
+// Epilogue reads and writes pass through small boxes in shared memory, a few
+// per warp, so that global accesses are whole rows of a box (64 or 128 bytes)
+// while each thread computes on its own row.  What is read (H; the addend)
+// comes ahead of the accumulator, what is written replaces it.  DOWN and DX,
+// one box in and out per warp and tile, move them by TMA (addend and result
+// at 18944 x 2048 x 256: 42 us; by the threads' own accesses 49).  DAP has two
+// in and three out, which by TMA queued behind the operand tiles' loads: its
+// threads move them (dA at 18944 x 2048 x 2048: 162 us; by TMA 183), and so
+// do UP's and DW's, for which it makes no difference.
 constexpr int PN = 256;                       // tile columns
 constexpr int PSTAGE = 2 * A_BYTES;
 constexpr int PART4 = BM * PN / 4;            // float4s of one CTA's partial
 constexpr int MAX_PAIRS = 74;
-constexpr int BOX = 4096;                     // 32 x 64 bf16, 128-byte swizzle
-constexpr int BOXW = 64;
+
+// A box: 32 rows of 16 * CPR bytes (CPR 16-byte chunks: 4 or 8), chunk c of
+// row r at chunk c ^ swizzle(r), so that a thread per row and a row per CPR
+// threads both spread over the banks.
+template <int CPR>
+__device__ __forceinline__ int box_off(int r, int c) {
+  return r * CPR * 16 + ((c ^ (CPR == 8 ? r & 7 : (r >> 1) & 3)) << 4);
+}
+// Columns 32 h .. of row `lane`.
+template <int CPR>
+__device__ __forceinline__ void box_get(const uint8_t* box, int lane, int h, uint4 (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const uint4*>(box + box_off<CPR>(lane, 4 * h + i));
+}
+template <int CPR>
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, int h, const float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+    uint4 u;
+    memcpy(&u, b, 16);
+    *reinterpret_cast<uint4*>(box + box_off<CPR>(lane, 4 * h + i)) = u;
+  }
+}
+// The warp copies a box to or from rows 0 .. rows - 1 and columns 0 .. cols - 1
+// (a multiple of 8; at most the box's) of p, rows ld elements apart.
+template <int CPR>
+__device__ __forceinline__ void box_load(uint8_t* box, const __nv_bfloat16* p, int64_t ld, int rows,
+                                         int cols, int lane) {
+  const int c = lane % CPR;
+#pragma unroll
+  for (int i = 0; i < CPR; ++i) {
+    const int r = i * (32 / CPR) + lane / CPR;
+    const bool ok = r < rows && c * 8 < cols;
+    cp_async16(box + box_off<CPR>(r, c), ok ? p + r * ld + c * 8 : p, ok);
+  }
+}
+template <int CPR>
+__device__ __forceinline__ void box_store(const uint8_t* box, __nv_bfloat16* p, int64_t ld, int rows,
+                                          int cols, int lane) {
+  const int c = lane % CPR;
+#pragma unroll
+  for (int i = 0; i < CPR; ++i) {
+    const int r = i * (32 / CPR) + lane / CPR;
+    if (r < rows && c * 8 < cols)
+      *reinterpret_cast<uint4*>(p + r * ld + c * 8) =
+          *reinterpret_cast<const uint4*>(box + box_off<CPR>(r, c));
+  }
+}
 
 template <int KIND> struct PCfg {
-  // boxes per epilogue warp: UP H1, H3 and A of its 64 columns; DAP the same,
-  // read and written in place; DOWN and DX a ring of three; DW two to store
-  static constexpr int BOXES = KIND == F_DW ? 2 : 3;
-  static constexpr int STAGES = KIND == F_DW ? 5 : 4;
-  static constexpr int SMEM = STAGES * PSTAGE + 8 * BOXES * BOX;
+  // Epilogue warps: 16 for DOWN and DX, whose K may be short (their way
+  // through a box is latency), else 8.
+  static constexpr int EW = KIND == F_DOWN || KIND == F_DX ? 16 : 8;
+  static constexpr int BLOCK = 64 + 32 * EW;
+  // Bytes of boxes per epilogue warp: UP H1, H3 and A of 64 columns; DAP two
+  // sets of H1 and H3 of 32 columns, replaced by dH, and one for A; DOWN and
+  // DX the addend of 64 columns, replaced by the result; DW 64 columns.
+  static constexpr int BOXB = KIND == F_UP ? 12288 : (KIND == F_DAP ? 10240 : 4096);
+  static constexpr int STAGES = KIND == F_DW ? 6 : (EW == 16 ? 5 : 4);
+  static constexpr int SMEM = STAGES * PSTAGE + EW * BOXB;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void epi_barrier() {   // the 8 epilogue warps
-  asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+template <int EW>
+__device__ __forceinline__ void epi_barrier() {   // the epilogue warps
+  asm volatile("bar.sync 1, %0;" ::"n"(EW * 32) : "memory");
 }
 
 // Columns 32 h .. of row `lane` of a box: 16-byte chunk c at chunk c ^ (lane & 7).
@@ -438,14 +510,14 @@ struct FWalk {
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__ FfnArgs a) {
+__global__ void __launch_bounds__(PCfg<KIND>::BLOCK, 1) k_ffn_pair(const __grid_constant__ FfnArgs a) {
   using C = PCfg<KIND>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[C::STAGES];    // used in the even CTA: both CTAs' bytes
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];        // used in the even CTA: both CTAs' warps
-  __shared__ __align__(8) uint64_t box_bar[8][3];        // per epilogue warp: a loaded box
+  __shared__ __align__(8) uint64_t box_bar[C::EW];       // TMA boxes: a warp's box has arrived
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ volatile int s_abort;
@@ -465,9 +537,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull_bar[s], 1);
-      mbar_init(&tempty_bar[s], 2 * (EPI_THREADS / 32));
+      mbar_init(&tempty_bar[s], 2 * C::EW);
     }
-    for (int i = 0; i < 24; ++i) mbar_init(&box_bar[i / 3][i % 3], 1);
+    for (int i = 0; i < C::EW; ++i) mbar_init(&box_bar[i], 1);
     fence_mbar_init();
     prefetch_tmap(&a.mA[0]);
     prefetch_tmap(&a.mB[0]);
@@ -493,7 +565,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
         const FTile ti = f_tile<KIND, PN, 2 * BM>(w.tile, a);
         const int m0 = ti.m0 + rank * BM;
         const int n0 = KIND == F_UP ? ti.n0 : ti.n0 + rank * (PN / 2);   // UP: W1 here, W3 there
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        // rows of different tiles start at different k-blocks, so that the loads
+        // in flight spread over the DRAM pages of a row; the weight gradients
+        // keep in step (all tiles read the same rows)
+        const int nkb = w.kb1 - w.kb0;
+        int kr = KIND == F_DW ? 0 : (ti.m0 / (2 * BM) * 5) % nkb;
+        for (int i = 0; i < nkb; ++i, kr = kr + 1 == nkb ? 0 : kr + 1) {
+          const int kb = w.kb0 + kr;
           if (!bounded_wait(&empty_bar[stage], phase ^ 1, &s_abort, a.status, 1, a.wait_ns))
             goto producer_done;
           uint8_t* sA = smem + stage * PSTAGE;
@@ -554,46 +632,66 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;                      // TMEM lane quarter of this warp
-    const int half = (warp - 2) >> 2;            // which half of the tile's columns
+    const int slice = (warp - 2) >> 2;           // which of SL slices of the tile's columns
+    constexpr int SL = C::EW / 4;
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-    uint8_t* boxes = smem + C::STAGES * PSTAGE + (warp - 2) * (C::BOXES * BOX);
-    constexpr int CH = (KIND == F_UP ? PN / 4 : PN / 2) / BOXW;   // boxes of a tile per warp
+    uint8_t* boxes = smem + C::STAGES * PSTAGE + (warp - 2) * C::BOXB;
+    constexpr int CPR = KIND == F_DAP ? 4 : 8;                    // 16-byte chunks of a box's row
+    constexpr int BOX = 512 * CPR, BOXW = 8 * CPR;                // a box's bytes and columns
+    constexpr int CH = (KIND == F_UP ? PN / 2 : PN) / SL / BOXW;  // boxes of a tile per warp
     constexpr bool READS = KIND == F_DAP || KIND == F_DOWN || KIND == F_DX;
-    constexpr int SETS = KIND == F_DAP ? 1 : C::BOXES;            // of the ring
+    constexpr bool TMA = KIND == F_DOWN || KIND == F_DX;
+    constexpr int SETS = KIND == F_DAP ? 2 : 1;                   // loaded ahead
     const bool rd = KIND == F_DAP || (READS && a.addend != nullptr);
-    uint64_t* bar = box_bar[warp - 2];
-    int it = 0, g = 0;                  // g: chunks so far; chunk g uses set g % SETS
-    // The loads run ahead of the accumulator on a walk of their own (lane 0).
+    int it = 0, g = 0;                  // g: boxes so far
+    // The loads run ahead of the accumulator on a walk of their own.
     FWalk wl(a, pair, npairs);
     int lj = CH, lg = 0, lrow = 0, lcol = 0;
-    auto load_next = [&]() {            // the next chunk's box(es) into set lg % SETS
+    auto load_next = [&]() {            // the addend's next box; H1's and H3's into set lg % SETS
+      bool more = true;
       if (lj == CH) {
-        if (!wl.next(a)) return;
-        const FTile ti = f_tile<KIND, PN, 2 * BM>(wl.tile, a);
-        lrow = ti.m0 + rank * BM + q * 32;
-        lcol = ti.n0 + half * CH * BOXW;
-        lj = 0;
-        // the ring does not cover HBM's latency: the next tile's boxes come to L2 now
-        FWalk wn = wl;
-        if (wn.next(a)) {
-          const FTile tn = f_tile<KIND, PN, 2 * BM>(wn.tile, a);
-          const int prow = tn.m0 + rank * BM + q * 32, pcol = tn.n0 + half * CH * BOXW;
-#pragma unroll
-          for (int i = 0; i < CH; ++i)
-            if (prow < a.M[0] && pcol + i * BOXW < a.N[0]) {
-              tma_prefetch_2d(&a.eI[0], pcol + i * BOXW, prow);
-              if (KIND == F_DAP) tma_prefetch_2d(&a.eI[1], pcol + i * BOXW, prow);
-            }
+        more = wl.next(a);
+        if (more) {
+          const FTile ti = f_tile<KIND, PN, 2 * BM>(wl.tile, a);
+          lrow = ti.m0 + rank * BM + q * 32;
+          lcol = ti.n0 + slice * CH * BOXW;
+          lj = 0;
         }
       }
-      const int set = lg % SETS;
-      mbar_arrive_expect_tx(&bar[set], KIND == F_DAP ? 2 * BOX : BOX);
-      tma_load_2d(boxes + set * BOX, &a.eI[0], &bar[set], lcol + lj * BOXW, lrow);
-      if (KIND == F_DAP) tma_load_2d(boxes + BOX, &a.eI[1], &bar[set], lcol + lj * BOXW, lrow);
-      ++lj;
-      ++lg;
+      if constexpr (TMA) {
+        if (lane == 0 && !a.dbg_no_load) {
+          bulk_wait_read_all();         // the result has left the box
+          if (more) {
+            mbar_arrive_expect_tx(&box_bar[warp - 2], BOX);
+            tma_load_2d(boxes, &a.eI, &box_bar[warp - 2], lcol, lrow);
+            // one box ahead does not cover HBM's latency: the next tile's comes to L2
+            FWalk wn = wl;
+            if (wn.next(a)) {
+              const FTile tn = f_tile<KIND, PN, 2 * BM>(wn.tile, a);
+              const int prow = tn.m0 + rank * BM + q * 32, pcol = tn.n0 + slice * CH * BOXW;
+              if (prow < a.M[0] && pcol < a.N[0]) tma_prefetch_2d(&a.eI, pcol, prow);
+            }
+          }
+        }
+        lj = CH;
+      } else {
+        if (more) {
+          const int rows = a.M[0] - lrow, cols = a.N[0] - lcol;
+          uint8_t* set = boxes + (lg % SETS) * 2 * BOX;
+          const __nv_bfloat16* p = a.hin + (size_t)lrow * 2 * a.f + lcol;
+          box_load<CPR>(set, p, 2 * a.f, rows, cols, lane);
+          box_load<CPR>(set + BOX, p + a.f, 2 * a.f, rows, cols, lane);
+          lcol += BOXW;
+          ++lj;
+          ++lg;
+        }
+        cp_async_commit();
+      }
     };
-    if (READS && rd && lane == 0 && !a.dbg_no_load) load_next();
+    if (READS && rd) {
+#pragma unroll
+      for (int i = 0; i < SETS; ++i) load_next();
+    }
     // Every epilogue warp walks every unit, also after a wait expired (the
     // waits then return at once): the barriers of shared tiles need all of them.
     for (FWalk w(a, pair, npairs); w.next(a); ++it) {
@@ -618,7 +716,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
         if (parts > 1) {
           float4* pb = partial(pair);
 #pragma unroll 1
-          for (int c = half * 4; c < half * 4 + 4; ++c) {
+          for (int c = slice * (8 / SL); c < (slice + 1) * (8 / SL); ++c) {
             uint32_t r[32];
             tmem_ld32(tbase + c * 32, r);
             tmem_ld_wait();
@@ -631,12 +729,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
             }
           }
           __threadfence();
-          epi_barrier();
+          epi_barrier<C::EW>();
           if (threadIdx.x == 64) {
             s_last = atomicAdd(&a.count[(w.tile - a.whole) * 2 + rank], 1) == parts - 1;
             __threadfence();
           }
-          epi_barrier();
+          epi_barrier<C::EW>();
           finish = s_last != 0;
         }
       }
@@ -665,23 +763,42 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
       };
 #pragma unroll 1
       for (int j = 0; j < CH; ++j, ++g) {
-        const int cb = (half * CH + j) * BOXW, col = ti.n0 + cb;
+        const int cb = (slice * CH + j) * BOXW, col = ti.n0 + cb;
         const bool inside = finish && col < N && row0 < M;   // else nothing of the box is stored
-        const int set = g % SETS;
-        uint8_t* box = boxes + set * BOX;
-        if (READS && rd) {
-          // the next chunk's box into the set whose result left two chunks ago
-          if (KIND != F_DAP && lane == 0) {
-            bulk_wait_read<1>();
-            if (!a.dbg_no_load) load_next();
+        const int rows = M - row0, cols = N - col;
+        uint8_t* box = boxes + (KIND == F_DAP ? (g % SETS) * 2 * BOX : 0);
+        if constexpr (TMA) {
+          static_assert(!TMA || CH == 1, "one box per warp and tile");
+          if (rd) {
+            bounded_wait(&box_bar[warp - 2], g & 1, &s_abort, a.status, 5, a.wait_ns);
+          } else {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
           }
-          bounded_wait(&bar[set], (g / SETS) & 1, &s_abort, a.status, 5, a.wait_ns);
-        } else {
-          // the box's (UP: the boxes') last results have left it
-          if (lane == 0) bulk_wait_read<KIND == F_UP ? 0 : SETS - 1>();
+        } else if (READS) {
+          cp_async_wait<SETS - 1>();
           __syncwarp();
         }
-        if (inside) {
+        if constexpr (KIND == F_DAP) {
+          if (inside) {
+            uint4 p1[4], p3[4];
+            box_get<CPR>(box, lane, 0, p1);
+            box_get<CPR>(box + BOX, lane, 0, p3);
+            chunk(cb / 32, v);
+            float d3[32], av[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              swiglu_bwd(v[i], bf16_lane(p1, i), bf16_lane(p3, i), v[i], d3[i], av[i]);
+            uint8_t* ab = boxes + 4 * BOX;
+            box_put<CPR>(box, lane, 0, v);
+            box_put<CPR>(box + BOX, lane, 0, d3);
+            box_put<CPR>(ab, lane, 0, av);
+            __syncwarp();
+            box_store<CPR>(box, a.out[0] + (size_t)row0 * a.ldo[0] + col, a.ldo[0], rows, cols, lane);
+            box_store<CPR>(box + BOX, a.out[1] + (size_t)row0 * a.ldo[1] + col, a.ldo[1], rows, cols, lane);
+            box_store<CPR>(ab, a.out[2] + (size_t)row0 * a.ldo[2] + col, a.ldo[2], rows, cols, lane);
+          }
+        } else if (inside) {
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int cc = cb / 32 + h;
@@ -690,74 +807,54 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_pair(const __grid_constant__
               chunk(cc, v);
               chunk(PN / 64 + cc, h3);
               if (a.save_h) {
-                box_put(boxes, lane, h, v);
-                box_put(boxes + BOX, lane, h, h3);
+                box_put<CPR>(boxes, lane, h, v);
+                box_put<CPR>(boxes + BOX, lane, h, h3);
               }
               // A from the accumulator, not from the rounded H: one rounding less
               // between x and y (2-norm error of y 2.4e-3 instead of 3.1e-3)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_fast(v[i]) * h3[i];
-              box_put(boxes + 2 * BOX, lane, h, v);
-            } else if constexpr (KIND == F_DAP) {
-              uint4 p1[4], p3[4];
-              box_get(boxes, lane, h, p1);
-              box_get(boxes + BOX, lane, h, p3);
-              chunk(cc, v);
-              float d3[32], av[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float h1 = bf16_lane(p1, i), h3 = bf16_lane(p3, i);
-                const float da = v[i];
-                const float sg = sigmoid_fast(h1);
-                const float sl = h1 * sg;
-                v[i] = da * h3 * (sg * (1.0f + h1 * (1.0f - sg)));
-                d3[i] = da * sl;
-                av[i] = sl * h3;
-              }
-              box_put(boxes, lane, h, v);
-              box_put(boxes + BOX, lane, h, d3);
-              box_put(boxes + 2 * BOX, lane, h, av);
+              for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid_ftz(v[i]) * h3[i];
+              box_put<CPR>(boxes + 2 * BOX, lane, h, v);
             } else {
-              uint4 p1[4];
-              if (READS && rd) box_get(box, lane, h, p1);
+              uint4 p1[4] = {};
+              if (READS && rd) box_get<CPR>(box, lane, h, p1);
               chunk(cc, v);
               if (READS && rd) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += bf16_lane(p1, i);
               }
-              box_put(box, lane, h, v);
+              box_put<CPR>(box, lane, h, v);
             }
           }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (inside) {
-            if constexpr (KIND == F_UP || KIND == F_DAP) {
-              if (KIND == F_DAP || a.save_h) {
-                tma_store_2d(&a.sO[0], boxes, col, row0);
-                tma_store_2d(&a.sO[1], boxes + BOX, col, row0);
-              }
-              tma_store_2d(&a.sO[2], boxes + 2 * BOX, col, row0);
-            } else {
-              tma_store_2d(&a.sO[KIND == F_DW ? ti.p : 0], box, col, row0);
+          if constexpr (TMA) fence_proxy_async_smem();
+          __syncwarp();
+          if constexpr (KIND == F_UP) {
+            if (a.save_h) {
+              box_store<CPR>(boxes, a.out[0] + (size_t)row0 * a.ldo[0] + col, a.ldo[0], rows, cols, lane);
+              box_store<CPR>(boxes + BOX, a.out[1] + (size_t)row0 * a.ldo[1] + col, a.ldo[1], rows, cols, lane);
             }
-          }
-          bulk_commit();
-          if (KIND == F_DAP) {   // one set: the next boxes once these have been read
-            bulk_wait_read<0>();
-            if (!a.dbg_no_load) load_next();
+            box_store<CPR>(boxes + 2 * BOX, a.out[2] + (size_t)row0 * a.ldo[2] + col, a.ldo[2], rows, cols, lane);
+          } else if constexpr (TMA) {
+            if (lane == 0) {
+              tma_store_2d(&a.eO, box, col, row0);
+              bulk_commit();
+            }
+          } else {
+            const int o = KIND == F_DW ? ti.p : 0;
+            box_store<CPR>(box, a.out[o] + (size_t)row0 * a.ldo[o] + col, a.ldo[o], rows, cols, lane);
           }
         }
-        __syncwarp();
+        __syncwarp();      // the box has been read: it may be filled again
+        if (READS && !TMA) load_next();
       }
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_shared(smem_u32(&tempty_bar[acc]), 0));
+      if (TMA && rd) load_next();   // waits for the result to leave the box
     }
+    if (TMA && lane == 0) bulk_wait_all();   // the stores end before the CTA does
   }
 
-  if (warp >= 2 && lane == 0) bulk_wait_all();   // the stores end before the CTA does
   if (s_abort) {   // aborted: let copies and MMAs in flight land
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
@@ -778,14 +875,14 @@ const char* f_name(int kind) {
 }
 
 template <class K>
-int f_go(K kernel, const FfnArgs& a, int kind, int grid, int cluster, int smem, bool dependent,
-         cudaStream_t s) {
+int f_go(K kernel, const FfnArgs& a, int kind, int grid, int block, int cluster, int smem,
+         bool dependent, cudaStream_t s) {
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
     return cuda_fail(e, "ffn smem attribute");
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = THREADS;
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at;
@@ -833,31 +930,30 @@ FPlan f_plan(int kind, int T, int d, int f) {
   // Clocks, for comparison only.  A pair's k-block takes 700 (measured at
   // 8192 x 7168 x 2048; 512 of MMAs), a split CTA's what 64 bytes per clock
   // bring in.  Whole waves of pairs; the rest shared where that ends the wave
-  // earlier: a part's partial costs its way through L2, and shares under 12
-  // k-blocks have measured no gain.
+  // earlier.  A partial's way through L2 costs each part about 2000, in the
+  // unit that sums them.  Tiles cut alike keep their pairs on the same
+  // k-blocks, which the weight gradients' long operands, streaming from HBM,
+  // need (32768 x 1536 x 256: 75 us, with cuts anywhere 92); where fewer than
+  // two parts per tile fit, cuts anywhere are what is left.
   p.tiles = count_tiles(kind, d, f, T, 2 * BM, PN);
-  const int rem = p.tiles % MAX_PAIRS;
-  const int share = (rem * kbs + MAX_PAIRS - 1) / MAX_PAIRS;
+  const int rem = p.tiles % MAX_PAIRS, waves = p.tiles / MAX_PAIRS;
   p.whole = p.tiles;
-  int64_t best = (int64_t)((p.tiles + MAX_PAIRS - 1) / MAX_PAIRS) * kbs * 700;
-  if (share >= 12) {
-    p.span = kbs;
-    p.share = share;
-    // The weight gradients' operands are long and stream from HBM: all tiles
-    // cut at the same k-blocks read them together, which halves the traffic
-    // (32768 x 1536 x 256: 92 us with arbitrary cuts).
-    if (kind == F_DW) {
-      const int parts = MAX_PAIRS / rem;
-      p.share = (kbs + parts - 1) / parts;
-      p.span = (kbs + p.share - 1) / p.share * p.share;
-    }
-    const int64_t t = (int64_t)(p.tiles / MAX_PAIRS) * kbs * 700 + p.share * 700 + 6000;
+  int64_t best = (int64_t)(waves + (rem > 0)) * kbs * 700;
+  auto share = [&](int k, int span, int parts) {
+    const int64_t t = (int64_t)waves * kbs * 700 + k * 700 + 3000 + parts * 2000;
     if (t < best) {
       best = t;
-      p.whole -= rem;
-    } else {
-      p.share = 0;
+      p.whole = p.tiles - rem;
+      p.share = k;
+      p.span = span;
     }
+  };
+  if (rem > 0) {
+    for (int parts = 2; parts <= MAX_PAIRS / rem && parts <= kbs; ++parts) {
+      const int k = (kbs + parts - 1) / parts;
+      share(k, (kbs + k - 1) / k * k, parts);
+    }
+    if (2 * rem > MAX_PAIRS) share((rem * kbs + MAX_PAIRS - 1) / MAX_PAIRS, kbs, 3);
   }
   // Few tiles: clusters of at most 8 along K, all resident at once.
   for (int bn = 256; bn >= 128; bn /= 2) {
@@ -900,11 +996,14 @@ int f_launch(FfnArgs& a, bool dependent, cudaStream_t s) {
   if (p.split) {
     const int grid = p.tiles * p.cluster;
     return p.bn == 256
-               ? f_go(k_ffn_split<KIND, 256>, a, KIND, grid, p.cluster, FCfg<256>::SMEM, dependent, s)
-               : f_go(k_ffn_split<KIND, 128>, a, KIND, grid, p.cluster, FCfg<128>::SMEM, dependent, s);
+               ? f_go(k_ffn_split<KIND, 256>, a, KIND, grid, THREADS, p.cluster,
+                      FCfg<256>::SMEM, dependent, s)
+               : f_go(k_ffn_split<KIND, 128>, a, KIND, grid, THREADS, p.cluster,
+                      FCfg<128>::SMEM, dependent, s);
   }
   const int pairs = p.share || p.whole > MAX_PAIRS ? MAX_PAIRS : p.whole;
-  return f_go(k_ffn_pair<KIND>, a, KIND, 2 * pairs, 2, PCfg<KIND>::SMEM, dependent, s);
+  return f_go(k_ffn_pair<KIND>, a, KIND, 2 * pairs, PCfg<KIND>::BLOCK, 2, PCfg<KIND>::SMEM,
+              dependent, s);
 }
 
 // An MN-major operand [rows, cols]: one box of `atoms` 64-column blocks where
@@ -915,15 +1014,15 @@ int map_mn(CUtensorMap* m, const void* p, int cols, int rows, int ld, int atoms,
                   : make_map_2d(m, p, cols, rows, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B, ld);
 }
 
-// [rows, cols] at p, rows ld elements apart, in the epilogue's boxes.
-int box_map(CUtensorMap* m, const void* p, int cols, int rows, int ld) {
-  return make_map_2d(m, p, cols, rows, BOXW, 32, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+// A matrix in the epilogue's TMA boxes.
+int box_map(CUtensorMap* m, const void* p, int cols, int rows) {
+  return make_map_2d(m, p, cols, rows, 64, 32);
 }
-// Output i: [rows, cols] at p, rows ld elements apart.
-int set_out(FfnArgs& a, int i, void* p, int cols, int rows, int ld) {
+
+// Output i at p, rows ld elements apart.
+void set_out(FfnArgs& a, int i, void* p, int ld) {
   a.out[i] = (__nv_bfloat16*)p;
   a.ldo[i] = ld;
-  return box_map(&a.sO[i], p, cols, rows, ld);
 }
 
 }  // namespace
@@ -1014,11 +1113,9 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     if ((rc = map_mn(&a.mB[0], p.w1, f, d, f, atoms, &b4))) return rc;
     if ((rc = map_mn(&a.mB[1], p.w3, f, d, f, atoms, &b4))) return rc;
     a.b4 = b4;
-    if (H) {
-      if ((rc = set_out(a, 0, h, f, T, 2 * f))) return rc;
-      if ((rc = set_out(a, 1, h + f, f, T, 2 * f))) return rc;
-    }
-    if ((rc = set_out(a, 2, act, f, T, f))) return rc;
+    set_out(a, 0, h, 2 * f);
+    set_out(a, 1, H ? h + f : nullptr, 2 * f);
+    set_out(a, 2, act, f);
     if ((rc = call.go<F_UP>(a))) return rc;
   }
   {  // DOWN
@@ -1029,9 +1126,10 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, BM))) return rc;
     if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, b_cols<F_DOWN>(T, d, f) / 64, &b4))) return rc;
     a.b4 = b4;
+    set_out(a, 0, y, d);
+    if ((rc = box_map(&a.eO, y, d, T))) return rc;
     if (addend)
-      if ((rc = box_map(&a.eI[0], addend, d, T, d))) return rc;
-    if ((rc = set_out(a, 0, y, d, T, d))) return rc;
+      if ((rc = box_map(&a.eI, addend, d, T))) return rc;
     if ((rc = call.go<F_DOWN>(a))) return rc;
   }
   return MOE_OK;
@@ -1051,11 +1149,9 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.hin = (const __nv_bfloat16*)H;
     if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, BM))) return rc;
     if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, b_cols<F_DAP>(T, d, f)))) return rc;
-    if ((rc = box_map(&a.eI[0], a.hin, f, T, 2 * f))) return rc;
-    if ((rc = box_map(&a.eI[1], a.hin + f, f, T, 2 * f))) return rc;
-    if ((rc = set_out(a, 0, dh, f, T, 2 * f))) return rc;
-    if ((rc = set_out(a, 1, dh + f, f, T, 2 * f))) return rc;
-    if ((rc = set_out(a, 2, act, f, T, f))) return rc;
+    set_out(a, 0, dh, 2 * f);
+    set_out(a, 1, dh + f, 2 * f);
+    set_out(a, 2, act, f);
     if ((rc = call.go<F_DAP>(a))) return rc;
   }
   {  // DX
@@ -1068,9 +1164,10 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
       if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B, 2 * f))) return rc;
       if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, b_cols<F_DX>(T, d, f)))) return rc;
     }
+    set_out(a, 0, dx, d);
+    if ((rc = box_map(&a.eO, dx, d, T))) return rc;
     if (addend)
-      if ((rc = box_map(&a.eI[0], addend, d, T, d))) return rc;
-    if ((rc = set_out(a, 0, dx, d, T, d))) return rc;
+      if ((rc = box_map(&a.eI, addend, d, T))) return rc;
     if ((rc = call.go<F_DX>(a))) return rc;
   }
   {  // DW
@@ -1086,7 +1183,7 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
       if ((rc = map_mn(&a.mB[i], w[i].B, w[i].N, T, w[i].ldb, b_cols<F_DW>(T, d, f) / 64, &b4))) return rc;
       a.a4 |= (int)a4 << i;
       a.b4 |= (int)b4 << i;
-      if ((rc = set_out(a, i, w[i].o, w[i].N, w[i].M, w[i].N))) return rc;
+      set_out(a, i, w[i].o, w[i].N);
     }
     if ((rc = call.go<F_DW>(a))) return rc;
   }
