@@ -7,6 +7,7 @@ arithmetic happens in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -520,11 +521,21 @@ def moe_token_bwd(dX_rows, dS, x, w_gate, idx, gate, plan, router_grad=True, gat
 
 
 # ------------------------------------------------------------------ the block around the experts
+# These calls check their tensors (shape, dtype, device, contiguity) and raise
+# MoEError before anything is launched.
 _CODES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+_F32 = torch.float32
 
 
 def _bad(msg, code=MOE_ERR_INVALID_ARG):
     raise MoEError(code, msg)
+
+
+def _matrix(name, t):
+    """(rows, columns, dtype code) of a matrix of a supported dtype."""
+    if t.dim() != 2:
+        _bad(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    return (*t.shape, _code(name, t))
 
 
 def _code(name, t):
@@ -532,51 +543,67 @@ def _code(name, t):
     return c if c is not None else _bad(f"{name}: unsupported dtype {t.dtype}", MOE_ERR_UNSUPPORTED)
 
 
-def _check_arg(name, t, shape, dtype, device, rows=False):
-    """t has this shape, dtype and device and is contiguous (rows: or a matrix
-    of contiguous rows at a row stride)."""
-    if t.shape != shape:
-        _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        _bad(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        _bad(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous() and not (rows and t.numel() and (t.stride(1) == 1 or t.shape[1] == 1)
-                                      and t.stride(0) >= t.shape[1]):
-        _bad(f"{name}: must be contiguous" + (" along its rows" if rows else ""))
+def _arg(name, t, shape, dtype, device):
+    """t is contiguous and has this shape, dtype and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _bad(f"{name}: expected a contiguous {tuple(shape)} {dtype} tensor on {device}, got "
+             f"{tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
 
 
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(name, t, shape, dtype, device):
+    """The same, but rows may lie at a stride of at least their length; returns it."""
+    if t.is_contiguous():
+        _arg(name, t, shape, dtype, device)
+        return shape[1]
+    ld = t.stride(0) if t.shape[0] > 1 else shape[1]
+    if (t.shape != shape or t.dtype != dtype or t.device != device or ld < shape[1]
+            or (shape[1] > 1 and t.stride(1) != 1)):
+        _bad(f"{name}: expected a {tuple(shape)} {dtype} tensor of contiguous rows on {device}, got "
+             f"{tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+    return ld
 
 
-class _On:
-    """Runs a call on its tensors' device and the given stream: allocations
-    made inside belong to that stream, so their memory is not handed out
+def _elsewhere(t, stream):
+    """Whether a call needs another device or stream than the current ones."""
+    if not t.is_cuda:
+        _bad(f"tensors must be on a CUDA device, got {t.device}")
+    if stream is not None and stream.device != t.device:
+        _bad(f"stream of {stream.device}, tensors on {t.device}")
+    return stream is not None or t.device.index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _there(t, stream):
+    """The tensor's device and the given stream as the current ones: what a call
+    allocates there belongs to that stream, so its memory is not handed out
     again while the stream still uses it."""
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        yield
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            _bad(f"tensors must be on a CUDA device, got {device}")
-        self.dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.dev is not None:
-            self.dev.__enter__()
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        if self.dev is not None:
-            self.dev.__exit__(*exc)
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _out(o, name, shape, dtype, device):
+    t = o.get(name)
+    if t is None:
+        t = o[name] = torch.empty(shape, device=device, dtype=dtype)
+    else:
+        _arg(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _ws(ws, size, device):
+    if ws is None:
+        return torch.empty(size if size > 0 else 1, device=device, dtype=torch.uint8)
+    if ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
+        _bad(f"ws: expected a contiguous uint8 tensor on {device}")
+    return ws
 
 
 def moe_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None,
@@ -584,31 +611,34 @@ def moe_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rs
     """Layer norm over the rows of x [T, d]: returns (y [T, d], mean [T] f32,
     rstd [T] f32).  x may have a row stride; weight and bias [d] are bf16 or
     fp32 (one dtype for both), or None."""
-    if x.dim() != 2:
-        _bad(f"x: expected a matrix, got {x.dim()} dimensions")
-    T, d = x.shape
-    dev, dt = x.device, _code("x", x)
-    _check_arg("x", x, (T, d), x.dtype, dev, rows=True)
+    T, d, dt = _matrix("x", x)
+    dev = x.device
+    ldx = _rows("x", x, x.shape, x.dtype, dev)
+    wdt = MOE_F32
     wt = weight if weight is not None else bias
-    wdt = MOE_F32 if wt is None else _code("weight", wt)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _check_arg(name, t, (d,), wt.dtype, dev)
+    if wt is not None:
+        wdt = _code("weight", wt)
+        if weight is not None:
+            _arg("weight", weight, (d,), wt.dtype, dev)
+        if bias is not None:
+            _arg("bias", bias, (d,), wt.dtype, dev)
     if (mean is None) != (rstd is None):
         _bad("mean and rstd: pass both or neither")
-    with _On(dev, stream) as s:
-        if y is None:
-            y = torch.empty(T, d, device=dev, dtype=x.dtype)
-        else:
-            _check_arg("y", y, (T, d), x.dtype, dev)
-        if mean is None:
-            mean, rstd = torch.empty(2, T, device=dev, dtype=torch.float32).unbind(0)
-        else:
-            _check_arg("mean", mean, (T,), torch.float32, dev)
-            _check_arg("rstd", rstd, (T,), torch.float32, dev)
-        _check(lib().moe_layernorm_fwd(x.data_ptr(), _row_stride(x), _ptr(weight), _ptr(bias), T, d,
-                                       dt, wdt, eps, y.data_ptr(), mean.data_ptr(),
-                                       rstd.data_ptr(), s))
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return moe_layernorm_fwd(x, weight, bias, eps, y, mean, rstd)
+    if y is None:
+        y = torch.empty((T, d), device=dev, dtype=x.dtype)
+    else:
+        _arg("y", y, (T, d), x.dtype, dev)
+    if mean is None:
+        mean, rstd = torch.empty(T, device=dev, dtype=_F32), torch.empty(T, device=dev, dtype=_F32)
+    else:
+        _arg("mean", mean, (T,), _F32, dev)
+        _arg("rstd", rstd, (T,), _F32, dev)
+    _check(lib().moe_layernorm_fwd(x.data_ptr(), ldx, _ptr(weight), _ptr(bias), T, d, dt, wdt, eps,
+                                   y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                   _raw_stream(dev)))
     return y, mean, rstd
 
 
@@ -619,135 +649,131 @@ def moe_layernorm_bwd_workspace_size(T, d) -> int:
 def moe_layernorm_bwd(dy, x, weight, mean, rstd, addend=None, out=None, ws=None, stream=None):
     """Backward of moe_layernorm_fwd.  Returns dict dx [T, d] (+ addend),
     dweight, dbias [d] f32.  dy, x and addend may have row strides."""
-    if x.dim() != 2:
-        _bad(f"x: expected a matrix, got {x.dim()} dimensions")
-    T, d = x.shape
-    dev, dt = x.device, _code("x", x)
-    _check_arg("x", x, (T, d), x.dtype, dev, rows=True)
-    _check_arg("dy", dy, (T, d), x.dtype, dev, rows=True)
-    _check_arg("mean", mean, (T,), torch.float32, dev)
-    _check_arg("rstd", rstd, (T,), torch.float32, dev)
-    if addend is not None:
-        _check_arg("addend", addend, (T, d), x.dtype, dev, rows=True)
-    wdt = MOE_F32 if weight is None else _code("weight", weight)
+    T, d, dt = _matrix("x", x)
+    dev, shape = x.device, x.shape
+    ldx = _rows("x", x, shape, x.dtype, dev)
+    lddy = _rows("dy", dy, shape, x.dtype, dev)
+    ldadd = 0 if addend is None else _rows("addend", addend, shape, x.dtype, dev)
+    _arg("mean", mean, (T,), _F32, dev)
+    _arg("rstd", rstd, (T,), _F32, dev)
+    wdt = MOE_F32
     if weight is not None:
-        _check_arg("weight", weight, (d,), weight.dtype, dev)
+        wdt = _code("weight", weight)
+        _arg("weight", weight, (d,), weight.dtype, dev)
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return moe_layernorm_bwd(dy, x, weight, mean, rstd, addend, out, ws)
     o = dict(out) if out else {}
-    with _On(dev, stream) as s:
-        for name, shape, dtype in (("dx", (T, d), x.dtype), ("dweight", (d,), torch.float32),
-                                   ("dbias", (d,), torch.float32)):
-            if name not in o:
-                o[name] = torch.empty(shape, device=dev, dtype=dtype)
-            else:
-                _check_arg(name, o[name], shape, dtype, dev)
-        if ws is None:
-            ws = torch.empty(max(moe_layernorm_bwd_workspace_size(T, d), 1), device=dev,
-                             dtype=torch.uint8)
-        _check(lib().moe_layernorm_bwd(
-            dy.data_ptr(), _row_stride(dy), x.data_ptr(), _row_stride(x), _ptr(weight),
-            mean.data_ptr(), rstd.data_ptr(), _ptr(addend),
-            0 if addend is None else _row_stride(addend), T, d, dt, wdt, o["dx"].data_ptr(),
-            o["dweight"].data_ptr(), o["dbias"].data_ptr(), ws.data_ptr(), ws.numel(), s))
+    dx = _out(o, "dx", (T, d), x.dtype, dev)
+    dw, db = _out(o, "dweight", (d,), _F32, dev), _out(o, "dbias", (d,), _F32, dev)
+    ws = _ws(ws, lib().moe_layernorm_bwd_workspace_size(T, d), dev)
+    _check(lib().moe_layernorm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, _ptr(weight),
+                                   mean.data_ptr(), rstd.data_ptr(), _ptr(addend), ldadd, T, d, dt,
+                                   wdt, dx, dw, db, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return o
-
-
-def _check_dropout(x, rng):
-    dt = _code("x", x)
-    if not x.is_contiguous():
-        _bad("x: must be contiguous")
-    _check_arg("rng", rng, (2,), torch.int64, x.device)
-    return dt
 
 
 def moe_dropout_fwd(x, p, rng, residual=None, out=None, stream=None):
     """residual + dropout(x) (residual None: dropout(x)); x of any shape.
     rng: int64 [2] on the device, (seed, offset); the mask is a function of
     (seed, offset, element index) alone and is not stored."""
-    dt = _check_dropout(x, rng)
+    dt, dev = _code("x", x), x.device
+    _arg("x", x, x.shape, x.dtype, dev)
+    _arg("rng", rng, (2,), torch.int64, dev)
     if residual is not None:
-        _check_arg("residual", residual, x.shape, x.dtype, x.device)
-    with _On(x.device, stream) as s:
-        if out is None:
-            out = torch.empty_like(x)
-        else:
-            _check_arg("out", out, x.shape, x.dtype, x.device)
-        _check(lib().moe_dropout_fwd(x.data_ptr(), _ptr(residual), x.numel(), p, rng.data_ptr(), dt,
-                                     out.data_ptr(), s))
+        _arg("residual", residual, x.shape, x.dtype, dev)
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return moe_dropout_fwd(x, p, rng, residual, out)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _arg("out", out, x.shape, x.dtype, dev)
+    _check(lib().moe_dropout_fwd(x.data_ptr(), _ptr(residual), x.numel(), p, rng.data_ptr(), dt,
+                                 out.data_ptr(), _raw_stream(dev)))
     return out
 
 
 def moe_dropout_bwd(dout, p, rng, dx=None, stream=None):
     """Gradient of moe_dropout_fwd for its x (the residual's is dout itself)."""
-    dt = _check_dropout(dout, rng)
-    with _On(dout.device, stream) as s:
-        if dx is None:
-            dx = torch.empty_like(dout)
-        else:
-            _check_arg("dx", dx, dout.shape, dout.dtype, dout.device)
-        _check(lib().moe_dropout_bwd(dout.data_ptr(), dout.numel(), p, rng.data_ptr(), dt,
-                                     dx.data_ptr(), s))
+    dt, dev = _code("dout", dout), dout.device
+    _arg("dout", dout, dout.shape, dout.dtype, dev)
+    _arg("rng", rng, (2,), torch.int64, dev)
+    if _elsewhere(dout, stream):
+        with _there(dout, stream):
+            return moe_dropout_bwd(dout, p, rng, dx)
+    if dx is None:
+        dx = torch.empty_like(dout)
+    else:
+        _arg("dx", dx, dout.shape, dout.dtype, dev)
+    _check(lib().moe_dropout_bwd(dout.data_ptr(), dout.numel(), p, rng.data_ptr(), dt,
+                                 dx.data_ptr(), _raw_stream(dev)))
     return dx
 
 
-def _check_ffn(x, w1, w3, w2):
-    if x.dim() != 2 or w1.dim() != 2:
-        _bad("x and w1: expected matrices")
-    (T, d), f = x.shape, w1.shape[1]
-    dev, dt = x.device, _code("x", x)
-    for name, t, shape in (("x", x, (T, d)), ("w1", w1, (d, f)), ("w3", w3, (d, f)),
-                           ("w2", w2, (f, d))):
-        _check_arg(name, t, shape, x.dtype, dev)
-    return T, d, f, dev, dt
+def _ffn_args(x, w1, w3, w2):
+    T, d, dt = _matrix("x", x)
+    f = _matrix("w1", w1)[1]
+    dev, xt = x.device, x.dtype
+    _arg("x", x, (T, d), xt, dev)
+    _arg("w1", w1, (d, f), xt, dev)
+    _arg("w3", w3, (d, f), xt, dev)
+    _arg("w2", w2, (f, d), xt, dev)
+    return T, d, f, dt, dev
+
+
+def moe_shared_ffn_fwd_workspace_size(T, d, f, dtype=MOE_BF16) -> int:
+    return lib().moe_shared_ffn_fwd_workspace_size(T, d, f, dtype)
 
 
 def moe_shared_ffn_fwd(x, w1, w3, w2, addend=None, H=None, y=None, save=True, ws=None,
                        stream=None):
     """Dense gated FFN: returns (y [T, d] = A W2 + addend, H [T, 2f]); save
     False: H is not written and None is returned for it (serving)."""
-    T, d, f, dev, dt = _check_ffn(x, w1, w3, w2)
+    T, d, f, dt, dev = _ffn_args(x, w1, w3, w2)
     if addend is not None:
-        _check_arg("addend", addend, (T, d), x.dtype, dev)
-    with _On(dev, stream) as s:
-        if not save:
-            H = None
-        elif H is None:
-            H = torch.empty(T, 2 * f, device=dev, dtype=x.dtype)
-        else:
-            _check_arg("H", H, (T, 2 * f), x.dtype, dev)
-        if y is None:
-            y = torch.empty(T, d, device=dev, dtype=x.dtype)
-        else:
-            _check_arg("y", y, (T, d), x.dtype, dev)
-        if ws is None:
-            ws = torch.empty(max(lib().moe_shared_ffn_fwd_workspace_size(T, d, f, dt), 1),
-                             device=dev, dtype=torch.uint8)
-        _check(lib().moe_shared_ffn_fwd(x.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
-                                        _ptr(addend), T, d, f, dt, _ptr(H), y.data_ptr(),
-                                        ws.data_ptr(), ws.numel(), s))
+        _arg("addend", addend, (T, d), x.dtype, dev)
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return moe_shared_ffn_fwd(x, w1, w3, w2, addend, H, y, save, ws)
+    if not save:
+        H = None
+    elif H is None:
+        H = torch.empty((T, 2 * f), device=dev, dtype=x.dtype)
+    else:
+        _arg("H", H, (T, 2 * f), x.dtype, dev)
+    if y is None:
+        y = torch.empty((T, d), device=dev, dtype=x.dtype)
+    else:
+        _arg("y", y, (T, d), x.dtype, dev)
+    ws = _ws(ws, lib().moe_shared_ffn_fwd_workspace_size(T, d, f, dt), dev)
+    _check(lib().moe_shared_ffn_fwd(x.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
+                                    _ptr(addend), T, d, f, dt, _ptr(H), y.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return y, H
+
+
+def moe_shared_ffn_bwd_workspace_size(T, d, f, dtype=MOE_BF16) -> int:
+    return lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dtype)
 
 
 def moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend=None, out=None, ws=None, stream=None):
     """Backward of moe_shared_ffn_fwd.  Returns dict dx [T, d] (+ addend),
     dw1, dw3 [d, f], dw2 [f, d]."""
-    T, d, f, dev, dt = _check_ffn(x, w1, w3, w2)
-    _check_arg("dout", dout, (T, d), x.dtype, dev)
-    _check_arg("H", H, (T, 2 * f), x.dtype, dev)
+    T, d, f, dt, dev = _ffn_args(x, w1, w3, w2)
+    _arg("dout", dout, (T, d), x.dtype, dev)
+    _arg("H", H, (T, 2 * f), x.dtype, dev)
     if addend is not None:
-        _check_arg("addend", addend, (T, d), x.dtype, dev)
+        _arg("addend", addend, (T, d), x.dtype, dev)
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend, out, ws)
     o = dict(out) if out else {}
-    with _On(dev, stream) as s:
-        for name, shape in (("dx", (T, d)), ("dw1", (d, f)), ("dw3", (d, f)), ("dw2", (f, d))):
-            if name not in o:
-                o[name] = torch.empty(shape, device=dev, dtype=x.dtype)
-            else:
-                _check_arg(name, o[name], shape, x.dtype, dev)
-        if ws is None:
-            ws = torch.empty(max(lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dt), 1),
-                             device=dev, dtype=torch.uint8)
-        _check(lib().moe_shared_ffn_bwd(dout.data_ptr(), x.data_ptr(), w1.data_ptr(),
-                                        w3.data_ptr(), w2.data_ptr(), H.data_ptr(), _ptr(addend),
-                                        T, d, f, dt, o["dx"].data_ptr(), o["dw1"].data_ptr(),
-                                        o["dw3"].data_ptr(), o["dw2"].data_ptr(), ws.data_ptr(),
-                                        ws.numel(), s))
+    dx = _out(o, "dx", (T, d), x.dtype, dev)
+    dw1, dw3 = _out(o, "dw1", (d, f), x.dtype, dev), _out(o, "dw3", (d, f), x.dtype, dev)
+    dw2 = _out(o, "dw2", (f, d), x.dtype, dev)
+    ws = _ws(ws, lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dt), dev)
+    _check(lib().moe_shared_ffn_bwd(dout.data_ptr(), x.data_ptr(), w1.data_ptr(), w3.data_ptr(),
+                                    w2.data_ptr(), H.data_ptr(), _ptr(addend), T, d, f, dt, dx,
+                                    dw1, dw3, dw2, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return o

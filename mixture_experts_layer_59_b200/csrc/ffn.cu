@@ -15,6 +15,8 @@
 // is no row space: the tensor maps end at T, d and f, loads past them read
 // zeros and stores past them are clipped, so any T and any d, f that are
 // multiples of 8 (the 16-byte row strides TMA needs) work.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc_tile.cuh"
@@ -874,11 +876,19 @@ const char* f_name(int kind) {
   return n[kind];
 }
 
-template <class K>
-int f_go(K kernel, const FfnArgs& a, int kind, int grid, int block, int cluster, int smem,
-         bool dependent, cudaStream_t s) {
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
-    return cuda_fail(e, "ffn smem attribute");
+template <void (*KERNEL)(const FfnArgs)>
+int f_go(const FfnArgs& a, int kind, int grid, int block, int cluster, int smem, bool dependent,
+         cudaStream_t s) {
+  // the attribute holds for a device: set it before the kernel's first launch there
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    if (cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+      return cuda_fail(e, "ffn smem attribute");
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -893,7 +903,7 @@ int f_go(K kernel, const FfnArgs& a, int kind, int grid, int block, int cluster,
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   ProfScope _ps(f_name(kind), s);
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a)) return cuda_fail(e, "ffn");
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, KERNEL, a)) return cuda_fail(e, "ffn");
   return MOE_OK;
 }
 
@@ -975,8 +985,7 @@ FPlan f_plan(int kind, int T, int d, int f) {
 }
 
 template <int KIND>
-int f_launch(FfnArgs& a, bool dependent, cudaStream_t s) {
-  const FPlan p = f_plan(KIND, a.T, a.d, a.f);
+int f_launch(FfnArgs& a, const FPlan& p, bool dependent, cudaStream_t s) {
   a.status = status_ptr();
   a.wait_ns = WAIT_LIMIT_NS;
   a.dbg_no_load = 0;
@@ -996,14 +1005,14 @@ int f_launch(FfnArgs& a, bool dependent, cudaStream_t s) {
   if (p.split) {
     const int grid = p.tiles * p.cluster;
     return p.bn == 256
-               ? f_go(k_ffn_split<KIND, 256>, a, KIND, grid, THREADS, p.cluster,
-                      FCfg<256>::SMEM, dependent, s)
-               : f_go(k_ffn_split<KIND, 128>, a, KIND, grid, THREADS, p.cluster,
-                      FCfg<128>::SMEM, dependent, s);
+               ? f_go<k_ffn_split<KIND, 256>>(a, KIND, grid, THREADS, p.cluster, FCfg<256>::SMEM,
+                                              dependent, s)
+               : f_go<k_ffn_split<KIND, 128>>(a, KIND, grid, THREADS, p.cluster, FCfg<128>::SMEM,
+                                              dependent, s);
   }
   const int pairs = p.share || p.whole > MAX_PAIRS ? MAX_PAIRS : p.whole;
-  return f_go(k_ffn_pair<KIND>, a, KIND, 2 * pairs, PCfg<KIND>::BLOCK, 2, PCfg<KIND>::SMEM,
-              dependent, s);
+  return f_go<k_ffn_pair<KIND>>(a, KIND, 2 * pairs, PCfg<KIND>::BLOCK, 2, PCfg<KIND>::SMEM, dependent,
+                                s);
 }
 
 // An MN-major operand [rows, cols]: one box of `atoms` 64-column blocks where
@@ -1027,28 +1036,24 @@ void set_out(FfnArgs& a, int i, void* p, int ld) {
 
 }  // namespace
 
-// Partials and counters of the split tiles of a call's products (one region,
+// Partials and counters of the shared tiles of a call's products (one region,
 // used by one product after the other); the counters are zeroed first.
+namespace {
 struct FScratch {
+  FPlan plan[5];       // of the call's kinds
   size_t part_bytes = 0, counts = 0;
 };
 FScratch ffn_scratch(int T, int d, int f, bool bwd) {
   FScratch z;
-  const int fwd_kinds[] = {F_UP, F_DOWN}, bwd_kinds[] = {F_DAP, F_DX, F_DW};
-  for (int i = 0; i < (bwd ? 3 : 2); ++i) {
-    const FPlan p = f_plan(bwd ? bwd_kinds[i] : fwd_kinds[i], T, d, f);
-    if (p.split || p.share == 0) continue;
+  for (int k = bwd ? F_DAP : F_UP; k <= (bwd ? F_DW : F_DOWN); ++k) {
+    const FPlan p = z.plan[k] = f_plan(k, T, d, f);
+    if (p.share == 0) continue;
     z.part_bytes = (size_t)MAX_PAIRS * 2 * 2 * PART4 * sizeof(float4);
     z.counts += (size_t)(p.tiles - p.whole) * 2;
   }
   return z;
 }
-size_t ffn_scratch_bytes(int T, int d, int f, bool bwd) {
-  const FScratch z = ffn_scratch(T, d, f, bwd);
-  return z.part_bytes + align_up(z.counts * sizeof(int), 256);
-}
 
-namespace {
 // Hands the scratch out to the products of one call.
 struct FCall {
   FScratch z;
@@ -1074,26 +1079,30 @@ struct FCall {
     a.f = f;
     return a;
   }
+  bool pairs(int kind) const { return !z.plan[kind].split; }
+  // Columns of B that one CTA loads per stage.
+  int b_cols(int kind) const {
+    const FPlan& p = z.plan[kind];
+    const int n = p.split ? p.bn : PN / 2;
+    return kind == F_UP && p.split ? n / 2 : n;
+  }
   template <int KIND>
   int go(FfnArgs& a) {
-    const FPlan p = f_plan(KIND, T, d, f);
+    const FPlan& p = z.plan[KIND];
     a.part = (float4*)base;
     a.count = count;
     if (p.share) count += (p.tiles - p.whole) * 2;
     const bool dependent = !first;
     first = false;
-    return f_launch<KIND>(a, dependent, s);
+    return f_launch<KIND>(a, p, dependent, s);
   }
 };
-
-// Columns of B that one CTA loads per stage.
-template <int KIND>
-int b_cols(int T, int d, int f) {
-  const FPlan p = f_plan(KIND, T, d, f);
-  const int n = p.split ? p.bn : PN / 2;
-  return KIND == F_UP && p.split ? n / 2 : n;
-}
 }  // namespace
+
+size_t ffn_scratch_bytes(int T, int d, int f, bool bwd) {
+  const FScratch z = ffn_scratch(T, d, f, bwd);
+  return z.part_bytes + align_up(z.counts * sizeof(int), 256);
+}
 
 int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, void* scratch,
             cudaStream_t s) {
@@ -1108,7 +1117,7 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     a.kbs = (d + BK - 1) / BK;
     a.save_h = H != nullptr;
     __nv_bfloat16* h = (__nv_bfloat16*)H;
-    const int atoms = b_cols<F_UP>(T, d, f) / 64;
+    const int atoms = call.b_cols(F_UP) / 64;
     if ((rc = make_map_2d(&a.mA[0], p.x, d, T, 64, BM))) return rc;
     if ((rc = map_mn(&a.mB[0], p.w1, f, d, f, atoms, &b4))) return rc;
     if ((rc = map_mn(&a.mB[1], p.w3, f, d, f, atoms, &b4))) return rc;
@@ -1124,11 +1133,12 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     a.kbs = (f + BK - 1) / BK;
     a.addend = (const __nv_bfloat16*)addend;
     if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, BM))) return rc;
-    if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, b_cols<F_DOWN>(T, d, f) / 64, &b4))) return rc;
+    if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, call.b_cols(F_DOWN) / 64, &b4))) return rc;
     a.b4 = b4;
     set_out(a, 0, y, d);
-    if ((rc = box_map(&a.eO, y, d, T))) return rc;
-    if (addend)
+    if (call.pairs(F_DOWN))
+      if ((rc = box_map(&a.eO, y, d, T))) return rc;
+    if (addend && call.pairs(F_DOWN))
       if ((rc = box_map(&a.eI, addend, d, T))) return rc;
     if ((rc = call.go<F_DOWN>(a))) return rc;
   }
@@ -1148,7 +1158,7 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.kbs = (d + BK - 1) / BK;
     a.hin = (const __nv_bfloat16*)H;
     if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, BM))) return rc;
-    if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, b_cols<F_DAP>(T, d, f)))) return rc;
+    if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, call.b_cols(F_DAP)))) return rc;
     set_out(a, 0, dh, 2 * f);
     set_out(a, 1, dh + f, 2 * f);
     set_out(a, 2, act, f);
@@ -1162,11 +1172,12 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.addend = (const __nv_bfloat16*)addend;
     for (int h = 0; h < 2; ++h) {
       if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B, 2 * f))) return rc;
-      if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, b_cols<F_DX>(T, d, f)))) return rc;
+      if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, call.b_cols(F_DX)))) return rc;
     }
     set_out(a, 0, dx, d);
-    if ((rc = box_map(&a.eO, dx, d, T))) return rc;
-    if (addend)
+    if (call.pairs(F_DX))
+      if ((rc = box_map(&a.eO, dx, d, T))) return rc;
+    if (addend && call.pairs(F_DX))
       if ((rc = box_map(&a.eI, addend, d, T))) return rc;
     if ((rc = call.go<F_DX>(a))) return rc;
   }
@@ -1180,7 +1191,7 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
       a.M[i] = w[i].M;
       a.N[i] = w[i].N;
       if ((rc = map_mn(&a.mA[i], w[i].A, w[i].M, T, w[i].lda, BM / 64, &a4))) return rc;
-      if ((rc = map_mn(&a.mB[i], w[i].B, w[i].N, T, w[i].ldb, b_cols<F_DW>(T, d, f) / 64, &b4))) return rc;
+      if ((rc = map_mn(&a.mB[i], w[i].B, w[i].N, T, w[i].ldb, call.b_cols(F_DW) / 64, &b4))) return rc;
       a.a4 |= (int)a4 << i;
       a.b4 |= (int)b4 << i;
       set_out(a, i, w[i].o, w[i].N);

@@ -12,6 +12,8 @@
 // activations' type.
 #include <math.h>
 
+#include <cstring>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -19,15 +21,45 @@ namespace moe {
 
 namespace {
 
-// V elements moved as one access of at most 16 bytes.
+// V elements moved as one access of at most 16 bytes (fp32 parameters beside
+// bf16 rows: two), held as raw bits and converted where they are used.
+template <int BYTES> struct Bits;
+template <> struct Bits<2> { typedef uint16_t type; };
+template <> struct Bits<4> { typedef uint32_t type; };
+template <> struct Bits<8> { typedef uint2 type; };
+template <> struct Bits<16> { typedef uint4 type; };
+
 template <class T, int V>
-struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Pack {
-  T v[V];
+struct Pack {
+  static constexpr int BYTES = V * (int)sizeof(T);
+  static constexpr int UNIT = BYTES > 16 ? 16 : BYTES;
+  typename Bits<UNIT>::type raw[BYTES / UNIT];
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(raw)[j];
+    else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(raw)[j] << 16);
+  }
+  __device__ __forceinline__ void set(int j, float v) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float*>(raw)[j] = v;
+    } else {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      memcpy(reinterpret_cast<uint16_t*>(raw) + j, &h, 2);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < BYTES / UNIT; ++i)
+      reinterpret_cast<typename Bits<UNIT>::type*>(p)[i] = raw[i];
+  }
 };
 
 template <class T, int V>
 __device__ __forceinline__ Pack<T, V> ld_pack(const T* p) {
-  return *reinterpret_cast<const Pack<T, V>*>(p);
+  Pack<T, V> r;
+#pragma unroll
+  for (int i = 0; i < Pack<T, V>::BYTES / Pack<T, V>::UNIT; ++i)
+    r.raw[i] = reinterpret_cast<const typename Bits<Pack<T, V>::UNIT>::type*>(p)[i];
+  return r;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -73,7 +105,7 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
     const int c = (lin + i * G) * V;
     if (live && c < d) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) s += to_f(raw[i].v[j]);
+      for (int j = 0; j < V; ++j) s += raw[i].get(j);
     }
   }
   const float inv_d = 1.0f / (float)d;
@@ -85,7 +117,7 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
     if (live && c < d) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float e = to_f(raw[i].v[j]) - mu;
+        const float e = raw[i].get(j) - mu;
         s = fmaf(e, e, s);
       }
     }
@@ -103,12 +135,12 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
       Pack<T, V> o;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float e = (to_f(raw[i].v[j]) - mu) * rs;
-        if (w) e *= to_f(pw.v[j]);
-        if (b) e += to_f(pb.v[j]);
-        o.v[j] = from_f<T>(e);
+        float e = (raw[i].get(j) - mu) * rs;
+        if (w) e *= pw.get(j);
+        if (b) e += pb.get(j);
+        o.set(j, e);
       }
-      *reinterpret_cast<Pack<T, V>*>(yr + c) = o;
+      o.store(yr + c);
     }
   }
   if (lin == 0 && mean) {
@@ -174,7 +206,7 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       aw[i * V + j] = ab[i * V + j] = 0.f;
-      wv[i * V + j] = w && c < d ? to_f(pw.v[j]) : 1.f;
+      wv[i * V + j] = w && c < d ? pw.get(j) : 1.f;
     }
   }
   struct Row {
@@ -210,8 +242,8 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int q = i * V + j;
-          const float dyv = to_f(cur.dy[i].v[j]);
-          const float xh = (to_f(cur.x[i].v[j]) - cur.mu) * cur.rs;
+          const float dyv = cur.dy[i].get(j);
+          const float xh = (cur.x[i].get(j) - cur.mu) * cur.rs;
           const float g = dyv * wv[q];
           aw[q] = fmaf(dyv, xh, aw[q]);
           ab[q] += dyv;
@@ -242,13 +274,13 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
         Pack<T, V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float xh = (to_f(cur.x[i].v[j]) - cur.mu) * cur.rs;
-          const float g = to_f(cur.dy[i].v[j]) * wv[i * V + j];
+          const float xh = (cur.x[i].get(j) - cur.mu) * cur.rs;
+          const float g = cur.dy[i].get(j) * wv[i * V + j];
           float v = cur.rs * (g - s1 - xh * s2);
-          if (add) v += to_f(cur.add[i].v[j]);
-          o.v[j] = from_f<T>(v);
+          if (add) v += cur.add[i].get(j);
+          o.set(j, v);
         }
-        *reinterpret_cast<Pack<T, V>*>(dx + row * d + c) = o;
+        o.store(dx + row * d + c);
       }
     }
     cur = next;
