@@ -15,8 +15,6 @@
 // is no row space: the tensor maps end at T, d and f, loads past them read
 // zeros and stores past them are clipped, so any T and any d, f that are
 // multiples of 8 (the 16-byte row strides TMA needs) work.
-#include <atomic>
-
 #include "common.cuh"
 #include "internal.h"
 #include "tc_tile.cuh"
@@ -876,19 +874,10 @@ const char* f_name(int kind) {
   return n[kind];
 }
 
-template <void (*KERNEL)(const FfnArgs)>
+template <auto* KERNEL>
 int f_go(const FfnArgs& a, int kind, int grid, int block, int cluster, int smem, bool dependent,
          cudaStream_t s) {
-  // the attribute holds for a device: set it before the kernel's first launch there
-  static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
-    if (cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
-      return cuda_fail(e, "ffn smem attribute");
-    ready.fetch_or(bit, std::memory_order_release);
-  }
+  if (cudaError_t e = smem_limit<KERNEL>(smem)) return cuda_fail(e, "ffn smem attribute");
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;

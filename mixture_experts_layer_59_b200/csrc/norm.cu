@@ -5,17 +5,20 @@
 //   dx = rstd (g - mean(g) - xh mean(g xh)) (+ addend)
 //   dw = sum_t dy xh,  db = sum_t dy
 //
-// Both directions are bound by HBM: a row is read once into registers, its
-// statistics are taken there (fp32; the variance from the centred values, a
-// second pass over registers, so an offset does not cancel) and its result
-// leaves from the same registers.  Results are rounded once, to the
-// activations' type.
+// Both directions are bound by HBM: a row is read once, its statistics are
+// taken from registers (fp32; the variance from the centred values, a second
+// pass over registers, so an offset does not cancel) and its result leaves
+// from the same registers (backward: from shared memory).  Results are rounded
+// once, to the activations' type.  At these rates the instructions count: the
+// arithmetic runs on pairs (two fp32 per instruction).
 #include <math.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_tile.cuh"
 
 namespace moe {
 
@@ -34,33 +37,104 @@ struct Pack {
   static constexpr int BYTES = V * (int)sizeof(T);
   static constexpr int UNIT = BYTES > 16 ? 16 : BYTES;
   typename Bits<UNIT>::type raw[BYTES / UNIT];
-  __device__ __forceinline__ float get(int j) const {
-    if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(raw)[j];
-    else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(raw)[j] << 16);
-  }
-  __device__ __forceinline__ void set(int j, float v) {
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<float*>(raw)[j] = v;
-    } else {
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      memcpy(reinterpret_cast<uint16_t*>(raw) + j, &h, 2);
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-#pragma unroll
-    for (int i = 0; i < BYTES / UNIT; ++i)
-      reinterpret_cast<typename Bits<UNIT>::type*>(p)[i] = raw[i];
-  }
 };
 
-template <class T, int V>
-__device__ __forceinline__ Pack<T, V> ld_pack(const T* p) {
-  Pack<T, V> r;
+// A thread's share of a row: NV packs of V columns, computed on in pairs (of
+// neighbours; of two packs where V is 1).  Columns past the row read zero.
+template <class T, int V, int NV>
+struct Vals {
+  static constexpr int NP = NV * V / 2;   // pairs
+  static_assert(V > 1 || NV % 2 == 0, "packs of one come in pairs");
+  Pack<T, V> p[NV];
+  // pack i holds columns col + i * step ..
+  __device__ __forceinline__ void load(const T* row, int col, int step, int d) {
 #pragma unroll
-  for (int i = 0; i < Pack<T, V>::BYTES / Pack<T, V>::UNIT; ++i)
-    r.raw[i] = reinterpret_cast<const typename Bits<Pack<T, V>::UNIT>::type*>(p)[i];
-  return r;
-}
+    for (int i = 0; i < NV; ++i) {
+      const int c = col + i * step;
+#pragma unroll
+      for (int u = 0; u < Pack<T, V>::BYTES / Pack<T, V>::UNIT; ++u) {
+        typedef typename Bits<Pack<T, V>::UNIT>::type B;
+        p[i].raw[u] = c < d ? reinterpret_cast<const B*>(row + c)[u] : B{};
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int col, int step, int d) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = col + i * step;
+      if (c < d) {
+#pragma unroll
+        for (int u = 0; u < Pack<T, V>::BYTES / Pack<T, V>::UNIT; ++u)
+          reinterpret_cast<typename Bits<Pack<T, V>::UNIT>::type*>(row + c)[u] = p[i].raw[u];
+      }
+    }
+  }
+  __device__ __forceinline__ F2 pair(int m) const {
+    if constexpr (V == 1) {
+      return f2(one(p[2 * m]), one(p[2 * m + 1]));
+    } else {
+      const Pack<T, V>& k = p[m / (V / 2)];
+      const int j = m % (V / 2);
+      if constexpr (sizeof(T) == 4) {
+        const float* e = reinterpret_cast<const float*>(k.raw);
+        return f2(e[2 * j], e[2 * j + 1]);
+      } else {
+        return f2_from_bf16x2(reinterpret_cast<const uint32_t*>(k.raw)[j]);
+      }
+    }
+  }
+  __device__ __forceinline__ void set_pair(int m, F2 v) {
+    if constexpr (V == 1) {
+      const float2 t = f2_get(v);
+      put(p[2 * m], t.x);
+      put(p[2 * m + 1], t.y);
+    } else {
+      Pack<T, V>& k = p[m / (V / 2)];
+      const int j = m % (V / 2);
+      if constexpr (sizeof(T) == 4) {
+        const float2 t = f2_get(v);
+        float* e = reinterpret_cast<float*>(k.raw);
+        e[2 * j] = t.x;
+        e[2 * j + 1] = t.y;
+      } else {
+        reinterpret_cast<uint32_t*>(k.raw)[j] = f2_to_bf16x2(v);
+      }
+    }
+  }
+  // Values derived from this share before and after this point are computed
+  // anew rather than kept in registers.
+  __device__ __forceinline__ void forget() {
+    constexpr int WORDS = NV * Pack<T, V>::BYTES / 4;
+    if constexpr (WORDS * 4 == NV * Pack<T, V>::BYTES && Pack<T, V>::UNIT >= 4) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) asm volatile("" : "+r"(w[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        asm volatile("" : "+h"(*reinterpret_cast<uint16_t*>(p[i].raw)));
+    }
+  }
+  // column of pair m's first (h = 0) or second element
+  __device__ __forceinline__ static int column(int m, int h, int col, int step) {
+    if (V == 1) return col + (2 * m + h) * step;
+    return col + m / (V > 1 ? V / 2 : 1) * step + 2 * (m % (V > 1 ? V / 2 : 1)) + h;
+  }
+
+ private:
+  __device__ __forceinline__ static float one(const Pack<T, V>& k) {
+    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float*>(k.raw);
+    else return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(k.raw) << 16);
+  }
+  __device__ __forceinline__ static void put(Pack<T, V>& k, float v) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float*>(k.raw) = v;
+    } else {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      memcpy(k.raw, &h, 2);
+    }
+  }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -80,68 +154,70 @@ __device__ __forceinline__ float group_sum(float v, float* red, int wpr, int war
   return s;
 }
 
+constexpr int LN_SMS = 148;
+
 // ============================================================== forward
-// A group of wpr warps holds one row: NV packs of V elements per thread.
-template <class T, class W, int V, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+// A group of WPR warps holds one row: NV packs of V elements per thread.
+// 16384 x 2048 bf16: 29 us, 4.6 TB/s (a plain copy of that size 25 us).
+template <class T, class W, int V, int NV, int WPR>
+__global__ void __launch_bounds__(WPR > 8 ? 1024 : 256)
 k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
-         float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float eps, int wpr) {
+         float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float inv_d, float eps) {
   __shared__ float red[2][32];
+  constexpr int wpr = WPR;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rpb = (blockDim.x >> 5) / wpr;
   const int64_t row = (int64_t)blockIdx.x * rpb + warp / wpr;
   const int lin = (warp % wpr) * 32 + lane, G = wpr * 32;
   const bool live = row < T_;
-  const T* xr = x + row * ldx;
-  Pack<T, V> raw[NV];
-  float s = 0.f;
+  typedef Vals<T, V, NV> X;
+  const F2 zero = f2(0.f, 0.f);
+  const int col = lin * V, step = G * V;
+  X raw;
+  raw.load(x + row * ldx, col, step, live ? d : 0);
+  F2 v[X::NP], acc = zero;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lin + i * G) * V;
-    if (live && c < d) raw[i] = ld_pack<T, V>(xr + c);
+  for (int m = 0; m < X::NP; ++m) {
+    v[m] = raw.pair(m);
+    acc = f2_add(acc, v[m]);
   }
+  const float2 a1 = f2_get(acc);
+  const float mu = group_sum(a1.x + a1.y, red[0], wpr, warp, lane) * inv_d;
+  const F2 nmu = f2(-mu, -mu);
+  acc = zero;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lin + i * G) * V;
-    if (live && c < d) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += raw[i].get(j);
+  for (int m = 0; m < X::NP; ++m) {
+    v[m] = f2_add(v[m], nmu);
+    if constexpr (V == 1) {
+      const float2 t = f2_get(v[m]);
+      v[m] = f2(X::column(m, 0, col, step) < d ? t.x : 0.f, X::column(m, 1, col, step) < d ? t.y : 0.f);
+    } else if (X::column(m, 0, col, step) >= d) {
+      v[m] = zero;
     }
+    acc = f2_fma(v[m], v[m], acc);
   }
-  const float inv_d = 1.0f / (float)d;
-  const float mu = group_sum(s, red[0], wpr, warp, lane) * inv_d;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lin + i * G) * V;
-    if (live && c < d) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float e = raw[i].get(j) - mu;
-        s = fmaf(e, e, s);
-      }
-    }
-  }
-  const float rs = 1.0f / sqrtf(group_sum(s, red[1], wpr, warp, lane) * inv_d + eps);
+  const float2 a2 = f2_get(acc);
+  const float rs = rsqrtf(group_sum(a2.x + a2.y, red[1], wpr, warp, lane) * inv_d + eps);
   if (!live) return;
-  T* yr = y + row * d;
+  const F2 rs2 = f2(rs, rs);
+  // the parameters pack by pack (of pairs of packs where V is 1): few registers
+  constexpr int PG = V == 1 ? 2 : 1;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lin + i * G) * V;
-    if (c < d) {
-      Pack<W, V> pw, pb;
-      if (w) pw = ld_pack<W, V>(w + c);
-      if (b) pb = ld_pack<W, V>(b + c);
-      Pack<T, V> o;
+  for (int i = 0; i < NV; i += PG) {
+    const int c = col + i * step;
+    Vals<W, V, PG> pw, pb;
+    Vals<T, V, PG> o;
+    if (w) pw.load(w, c, step, d);
+    if (b) pb.load(b, c, step, d);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float e = (raw[i].get(j) - mu) * rs;
-        if (w) e *= pw.get(j);
-        if (b) e += pb.get(j);
-        o.set(j, e);
-      }
-      o.store(yr + c);
+    for (int j = 0; j < Vals<T, V, PG>::NP; ++j) {
+      F2 e = f2_mul(v[i / PG * Vals<T, V, PG>::NP + j], rs2);
+      if (w && b) e = f2_fma(e, pw.pair(j), pb.pair(j));
+      else if (w) e = f2_mul(e, pw.pair(j));
+      else if (b) e = f2_add(e, pb.pair(j));
+      o.set_pair(j, e);
     }
+    o.store(y + row * d, c, step, d);
   }
   if (lin == 0 && mean) {
     mean[row] = mu;
@@ -168,7 +244,7 @@ k_ln_fwd_wide(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restr
     const float e = to_f(xr[c]) - mu;
     s = fmaf(e, e, s);
   }
-  const float rs = 1.0f / sqrtf(group_sum(s, red[1], 32, warp, lane) * inv_d + eps);
+  const float rs = rsqrtf(group_sum(s, red[1], 32, warp, lane) * inv_d + eps);
   for (int64_t c = threadIdx.x; c < d; c += blockDim.x) {
     float e = (to_f(xr[c]) - mu) * rs;
     if (w) e *= to_f(w[c]);
@@ -182,120 +258,313 @@ k_ln_fwd_wide(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restr
 }
 
 // ============================================================== backward
-// A block walks rows; a group of G threads owns one row at a time and each
-// thread the same columns of every row (NV packs of V), so that the column
-// sums of dy xh and dy stay in registers until the block's last row and
-// leave as one partial row per group.  The next row's loads are issued
-// before this row's two sums are taken.
-template <class T, class W, int V, int NV, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB)
+// Any rows of up to 8192 columns.  A block walks rows; a group of G threads
+// owns a row at a time and each thread the same 8 columns of every row, so
+// that the column sums of dy xh and dy stay in registers until the block's
+// last row and leave as one partial row per block.
+template <class T, class W, int V, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 512 / MAXT : 1)
 k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
          const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
-         int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, int G) {
+         int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, float inv_d, int G) {
+  extern __shared__ float colsum[];        // [2][d], where a block has several groups
   __shared__ float2 red[2][32];
+  constexpr int NV = 8 / V;
+  typedef Vals<T, V, NV> X;
+  constexpr int PG = V == 1 ? 2 : 1, GP = X::NP / (NV / PG);   // pairs of PG packs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = threadIdx.x / G, lin = threadIdx.x - grp * G;
-  const int rpb = blockDim.x / G, wpg = G >> 5;
-  const float inv_d = 1.0f / (float)d;
-  float aw[NV * V], ab[NV * V], wv[NV * V];
+  const int groups = blockDim.x / G, wpg = G >> 5;
+  const int col = lin * V, step = G * V;
+  const F2 zero = f2(0.f, 0.f), one = f2(1.f, 1.f);
+  F2 aw[X::NP], ab[X::NP];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lin + i * G) * V;
-    Pack<W, V> pw;
-    if (w && c < d) pw = ld_pack<W, V>(w + c);
+  for (int m = 0; m < X::NP; ++m) aw[m] = ab[m] = zero;
+  int64_t row = (int64_t)blockIdx.x * groups + grp;
+  const int64_t rstep = (int64_t)gridDim.x * groups;
+  for (int it = 0; (int64_t)blockIdx.x * groups + it * rstep < T_; ++it, row += rstep) {
+    // a row past the last has no columns: zeros
+    const int dd = row < T_ ? d : 0;
+    X vx, vd, va;
+    vx.load(x + row * ldx, col, step, dd);
+    vd.load(dy + row * lddy, col, step, dd);
+    if (add) va.load(add + row * ldadd, col, step, dd);
+    const float mu = dd ? mean[row] : 0.f, r = dd ? rstd[row] : 0.f;
+    const F2 nmu = f2(-mu, -mu), rs = f2(r, r);
+    // columns past the row have dy = 0 and add nothing to the sums
+    F2 t1 = zero, t2 = zero;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      aw[i * V + j] = ab[i * V + j] = 0.f;
-      wv[i * V + j] = w && c < d ? pw.get(j) : 1.f;
-    }
-  }
-  struct Row {
-    Pack<T, V> x[NV], dy[NV], add[NV];
-    float mu, rs;
-  };
-  auto load = [&](Row& q, int64_t row) {
-    if (row < T_) {
+    for (int i = 0; i < NV / PG; ++i) {
+      Vals<W, V, PG> pw;
+      if (w) pw.load(w, col + i * PG * step, step, d);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (lin + i * G) * V;
-        if (c < d) {
-          q.x[i] = ld_pack<T, V>(x + row * ldx + c);
-          q.dy[i] = ld_pack<T, V>(dy + row * lddy + c);
-          if (add) q.add[i] = ld_pack<T, V>(add + row * ldadd + c);
-        }
-      }
-      q.mu = mean[row];
-      q.rs = rstd[row];
-    }
-  };
-  int64_t row = (int64_t)blockIdx.x * rpb + grp;
-  const int64_t step = (int64_t)gridDim.x * rpb;
-  Row cur, next;
-  load(cur, row);
-  for (int it = 0; (int64_t)blockIdx.x * rpb + it * step < T_; ++it, row += step) {
-    const bool live = row < T_;
-    load(next, row + step);
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (live && (lin + i * G) * V < d) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int q = i * V + j;
-          const float dyv = cur.dy[i].get(j);
-          const float xh = (cur.x[i].get(j) - cur.mu) * cur.rs;
-          const float g = dyv * wv[q];
-          aw[q] = fmaf(dyv, xh, aw[q]);
-          ab[q] += dyv;
-          s1 += g;
-          s2 = fmaf(g, xh, s2);
-        }
+      for (int j = 0; j < GP; ++j) {
+        const int m = i * GP + j;
+        const F2 dyv = vd.pair(m);
+        const F2 xh = f2_mul(f2_add(vx.pair(m), nmu), rs);
+        const F2 g = w ? f2_mul(dyv, pw.pair(j)) : dyv;
+        aw[m] = f2_fma(dyv, xh, aw[m]);
+        ab[m] = f2_add(ab[m], dyv);
+        t1 = f2_add(t1, g);
+        t2 = f2_fma(g, xh, t2);
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (wpg > 1) {
-      float2* rb = red[it & 1];      // two buffers: one barrier per row
-      if (lane == 0) rb[warp] = make_float2(s1, s2);
+    const float2 p1 = f2_get(t1), p2 = f2_get(t2);
+    // both sums over the warp: each half goes on with one
+    const bool hi = lane & 16;
+    const float u1 = p1.x + p1.y, u2 = p2.x + p2.y;
+    float u = (hi ? u2 : u1) + __shfl_xor_sync(0xffffffffu, hi ? u1 : u2, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    float s1 = __shfl_sync(0xffffffffu, u, 0), s2 = __shfl_sync(0xffffffffu, u, 16);
+    if (wpg > 1) {                         // two buffers: one barrier per row
+      if (lane == 0) red[it & 1][warp] = make_float2(s1, s2);
       __syncthreads();
       s1 = s2 = 0.f;
       for (int i = 0; i < wpg; ++i) {
-        const float2 v = rb[grp * wpg + i];
+        const float2 v = red[it & 1][grp * wpg + i];
         s1 += v.x;
         s2 += v.y;
       }
     }
-    s1 *= inv_d;
-    s2 *= inv_d;
+    const F2 ns1 = f2(-s1 * inv_d, -s1 * inv_d), ns2 = f2(-s2 * inv_d, -s2 * inv_d);
+    vx.forget();
+    vd.forget();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lin + i * G) * V;
-      if (live && c < d) {
-        Pack<T, V> o;
+    for (int i = 0; i < NV / PG; ++i) {
+      Vals<W, V, PG> pw;
+      if (w) pw.load(w, col + i * PG * step, step, d);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float xh = (cur.x[i].get(j) - cur.mu) * cur.rs;
-          const float g = cur.dy[i].get(j) * wv[i * V + j];
-          float v = cur.rs * (g - s1 - xh * s2);
-          if (add) v += cur.add[i].get(j);
-          o.set(j, v);
-        }
-        o.store(dx + row * d + c);
+      for (int j = 0; j < GP; ++j) {
+        const int m = i * GP + j;
+        const F2 xh = f2_mul(f2_add(vx.pair(m), nmu), rs);
+        const F2 e = f2_fma(xh, ns2, f2_fma(vd.pair(m), w ? pw.pair(j) : one, ns1));
+        vx.set_pair(m, add ? f2_fma(e, rs, va.pair(m)) : f2_mul(e, rs));
       }
     }
-    cur = next;
+    vx.store(dx + row * d, col, step, dd);
   }
   if (part == nullptr) return;
-  float* pr = part + ((size_t)blockIdx.x * rpb + grp) * 2 * d;
+  // the groups' sums, added in order
+  float* pr = part + (size_t)blockIdx.x * 2 * d;
+  for (int k = 0; k < groups; ++k) {
+    if (grp == k) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lin + i * G) * V;
+      for (int m = 0; m < X::NP; ++m) {
+        const float2 sw = f2_get(aw[m]), sb = f2_get(ab[m]);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (c + j < d) {
-        pr[c + j] = aw[i * V + j];
-        pr[d + c + j] = ab[i * V + j];
+        for (int h = 0; h < 2; ++h) {
+          const int c = X::column(m, h, col, step);
+          if (c < d) {
+            float u = h ? sw.y : sw.x, v = h ? sb.y : sb.x;
+            if (k > 0) {
+              u += colsum[c];
+              v += colsum[d + c];
+            }
+            float* to = k == groups - 1 ? pr : colsum;
+            to[c] = u;
+            to[d + c] = v;
+          }
+        }
       }
+    }
+    if (groups > 1) __syncthreads();
+  }
+}
+
+// Many rows of 16-byte units.  The same sums in three roles that never meet at
+// a barrier of the block, so that the loads, the rows' sums and the columns'
+// sums of different rows overlap: one thread brings stages of R rows by bulk
+// copies; four warps take each row's two sums over its columns; eight warps,
+// a thread to the same columns of all rows, take rows to dx and to the column
+// sums in their registers.  (The kernel above, whose warps all wait for each
+// row's sums, 86 us at 32768 x 1536 bf16 with an addend; with all 8 warps
+// first at the rows' sums, then at the columns, 87; this one 74 and 4 for the
+// partial rows' sums: 5.4 TB/s; a plain sum of two such tensors runs at 6.5.)
+constexpr int LN_CW = 8, LN_SW = 4;              // column warps, row-sum warps
+constexpr int LN_WS_THREADS = 32 * (LN_CW + LN_SW + 1);
+constexpr int LN_STAGES = 6;                     // at most
+
+template <class T, class W, int NPK>   // NPK: 16-byte packs of a row per column thread
+__global__ void __launch_bounds__(LN_WS_THREADS, NPK == 1 ? 2 : 1)
+k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
+            const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
+            int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, float inv_d, int R,
+            int stages, int ct, int* status) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[LN_STAGES], ready[LN_STAGES], empty[LN_STAGES];
+  // per row of a stage, as pairs of the same value: -mean, rstd, -s1 / d, -s2 / d
+  __shared__ __align__(16) F2 stat[LN_STAGES][8][4];
+  __shared__ volatile int s_abort;
+  constexpr int V = 16 / (int)sizeof(T), HV = V / 2;
+  typedef Vals<T, V, 1> P;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rb = (uint32_t)d * sizeof(T);
+  const int na = add ? 3 : 2;
+  const uint32_t stage_bytes = (uint32_t)(na * R) * rb;
+  const int64_t tiles = ((int64_t)T_ + R - 1) / R;
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < LN_STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&ready[i], LN_SW);
+      mbar_init(&empty[i], LN_CW);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  int st = 0;
+  uint32_t phase = 0;
+  auto advance = [&]() {
+    if (++st == stages) { st = 0; phase ^= 1; }
+  };
+  auto rows_of = [&](int64_t t) { return (int)(T_ - t * R < R ? T_ - t * R : R); };
+  if (warp == LN_CW + LN_SW) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
+        if (!bounded_wait(&empty[st], phase ^ 1, &s_abort, status, 6, WAIT_LIMIT_NS)) break;
+        const int rows = rows_of(t);
+        mbar_arrive_expect_tx(&full[st], (uint32_t)(na * rows) * rb);
+        uint8_t* base = smem + (size_t)st * stage_bytes;
+        for (int r = 0; r < rows; ++r) {
+          const int64_t row = t * R + r;
+          bulk_load(base + (size_t)r * rb, x + row * ldx, rb, &full[st]);
+          bulk_load(base + (size_t)(R + r) * rb, dy + row * lddy, rb, &full[st]);
+          if (add) bulk_load(base + (size_t)(2 * R + r) * rb, add + row * ldadd, rb, &full[st]);
+        }
+      }
+    }
+  } else if (warp >= LN_CW) {
+    // ------------------------------------------------------------ the rows' sums
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
+      const int rows = rows_of(t);
+      const uint8_t* base = smem + (size_t)st * stage_bytes;
+      const int64_t r0 = t * R + warp - LN_CW;   // this warp's first row: its statistics early
+      const bool any = warp - LN_CW < rows;
+      const float mu0 = any ? mean[r0] : 0.f, rs0 = any ? rstd[r0] : 0.f;
+      // a warp without a row waits too: it must not run ahead of the stage
+      bounded_wait(&full[st], phase, &s_abort, status, 7, WAIT_LIMIT_NS);
+      for (int r = warp - LN_CW; r < rows; r += LN_SW) {
+        const bool first = r == warp - LN_CW;
+        const float mu = first ? mu0 : mean[t * R + r], rs = first ? rs0 : rstd[t * R + r];
+        const F2 nmu = f2(-mu, -mu);
+        const T* xr = reinterpret_cast<const T*>(base + (size_t)r * rb);
+        const T* dr = reinterpret_cast<const T*>(base + (size_t)(R + r) * rb);
+        F2 t1 = f2(0.f, 0.f), t2 = t1;
+#pragma unroll 4
+        for (int c = lane * V; c < d; c += 32 * V) {
+          P px, pd;
+          Vals<W, V, 1> pw;
+          px.load(xr, c, 0, d);
+          pd.load(dr, c, 0, d);
+          if (w) pw.load(w, c, 0, d);
+#pragma unroll
+          for (int j = 0; j < HV; ++j) {
+            const F2 g = w ? f2_mul(pd.pair(j), pw.pair(j)) : pd.pair(j);
+            t1 = f2_add(t1, g);
+            t2 = f2_fma(g, f2_add(px.pair(j), nmu), t2);   // rstd times this: sum g xh
+          }
+        }
+        const float2 p1 = f2_get(t1), p2 = f2_get(t2);
+        const float s1 = warp_sum(p1.x + p1.y) * inv_d, s2 = warp_sum(p2.x + p2.y) * rs * inv_d;
+        if (lane == 0) {
+          stat[st][r][0] = f2(-mu, -mu);
+          stat[st][r][1] = f2(rs, rs);
+          stat[st][r][2] = f2(-s1, -s1);
+          stat[st][r][3] = f2(-s2, -s2);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[st]);
+    }
+  } else {
+    // ------------------------------------------------------------ dx and the columns' sums
+    // ct threads side by side cover a row's packs; the others take other rows
+    const int sg = threadIdx.x / ct, c0 = (threadIdx.x % ct) * V, cstep = ct * V;
+    const int nsg = 32 * LN_CW / ct;
+    F2 aw[NPK * HV], ab[NPK * HV], wv[NPK * HV];
+#pragma unroll
+    for (int i = 0; i < NPK; ++i) {
+      Vals<W, V, 1> pw;
+      if (w) pw.load(w, c0 + i * cstep, 0, d);
+#pragma unroll
+      for (int j = 0; j < HV; ++j) {
+        aw[i * HV + j] = ab[i * HV + j] = f2(0.f, 0.f);
+        wv[i * HV + j] = w ? pw.pair(j) : f2(1.f, 1.f);
+      }
+    }
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
+      const int rows = rows_of(t);
+      const uint8_t* base = smem + (size_t)st * stage_bytes;
+      bounded_wait(&ready[st], phase, &s_abort, status, 8, WAIT_LIMIT_NS);
+#pragma unroll 2
+      for (int r = sg; r < rows; r += nsg) {
+        const F2 nmu = stat[st][r][0], rs2 = stat[st][r][1], ns1 = stat[st][r][2], ns2 = stat[st][r][3];
+        const T* xr = reinterpret_cast<const T*>(base + (size_t)r * rb);
+        const T* dr = reinterpret_cast<const T*>(base + (size_t)(R + r) * rb);
+        const T* ar = reinterpret_cast<const T*>(base + (size_t)(2 * R + r) * rb);
+        T* orow = dx + (t * R + r) * d;
+#pragma unroll
+        for (int i = 0; i < NPK; ++i) {
+          const int c = c0 + i * cstep;
+          if (c < d) {
+            P px, pd, pa, o;
+            px.load(xr, c, 0, d);
+            pd.load(dr, c, 0, d);
+            if (add) pa.load(ar, c, 0, d);
+#pragma unroll
+            for (int j = 0; j < HV; ++j) {
+              const int m = i * HV + j;
+              const F2 dyv = pd.pair(j);
+              const F2 xh = f2_mul(f2_add(px.pair(j), nmu), rs2);
+              aw[m] = f2_fma(dyv, xh, aw[m]);
+              ab[m] = f2_add(ab[m], dyv);
+              const F2 e = f2_fma(xh, ns2, f2_fma(dyv, wv[m], ns1));
+              o.set_pair(j, add ? f2_fma(e, rs2, pa.pair(j)) : f2_mul(e, rs2));
+            }
+            o.store(orow, c, 0, d);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    if (part != nullptr) {
+      // the row subgroups' sums, added in order; every stage has been read by
+      // then, so its memory holds them
+      auto columns = []() { asm volatile("bar.sync 1, %0;" ::"n"(32 * LN_CW) : "memory"); };
+      float* acc = reinterpret_cast<float*>(smem);   // [2][d]
+      float* pr = part + (size_t)blockIdx.x * 2 * d;
+      columns();
+      for (int k = 0; k < nsg; ++k) {
+        if (sg == k) {
+          float* to = k == nsg - 1 ? pr : acc;
+#pragma unroll
+          for (int m = 0; m < NPK * HV; ++m) {
+            const int c = c0 + m / HV * cstep + 2 * (m % HV);
+            if (c < d) {
+              float2 sw = f2_get(aw[m]), sb = f2_get(ab[m]);
+              if (k > 0) {
+                sw.x += acc[c];
+                sw.y += acc[c + 1];
+                sb.x += acc[d + c];
+                sb.y += acc[d + c + 1];
+              }
+              to[c] = sw.x;
+              to[c + 1] = sw.y;
+              to[d + c] = sb.x;
+              to[d + c + 1] = sb.y;
+            }
+          }
+        }
+        columns();
+      }
+    }
+  }
+  if (s_abort) {   // a wait expired: let copies in flight land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
 }
 
@@ -306,8 +575,10 @@ k_ln_reduce(const float* __restrict__ part, int nparts, int d, float* __restrict
             float* __restrict__ db) {
   __shared__ float sm[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  tc::grid_dependency_wait();
   float s = 0.f;
   if (c < 2 * (int64_t)d)
+#pragma unroll 8
     for (int r = threadIdx.y; r < nparts; r += 32) s += part[(size_t)r * 2 * d + c];
   sm[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -392,26 +663,36 @@ template <class T, class W, int V>
 int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, float eps, T* y,
              float* mean, float* rstd, cudaStream_t s) {
   const int npack = d / V;
-  // Warps per row: as few as hold the row in 8 packs a thread; more while
-  // the rows alone do not give the SMs 16 warps each (few rows: latency).
+  // Warps per row: as few as hold the row in 4 packs a thread (16384 x 2048
+  // bf16: 2 warps 36 us, 1 warp with 8 packs 44, 4 warps 38); more while the
+  // rows alone do not give the SMs 16 warps each (few rows: latency).  Rows
+  // past 32 warps of 4 take 8 packs.
   int wpr = 1;
-  while (wpr < 32 && npack > wpr * 32 * 8) wpr *= 2;
-  while (wpr < 32 && npack > wpr * 32 && (int64_t)T_ * wpr < 148 * 16) wpr *= 2;
+  while (wpr < 32 && npack > wpr * 32 * 4) wpr *= 2;
+  while (wpr < 32 && npack > wpr * 32 && (int64_t)T_ * wpr < LN_SMS * 16) wpr *= 2;
   const int nv = (npack + wpr * 32 - 1) / (wpr * 32);
-  const int warps = wpr > 8 ? wpr : 8;
-  const int rpb = warps / wpr;
-  const unsigned grid = (unsigned)(((int64_t)T_ + rpb - 1) / rpb);
+  const float inv_d = 1.0f / (float)d;
   ProfScope _ps("layernorm_fwd", s);
-#define LN_GO(NV, MAXT)                                                                        \
-  k_ln_fwd<T, W, V, NV, MAXT><<<grid, warps * 32, 0, s>>>(x, ldx, w, b, y, mean, rstd, T_, d,  \
-                                                          eps, wpr)
+#define LN_GO(NV, WPR)                                                                        \
+  do {                                                                                        \
+    const int rpb = WPR == 1 ? 2 : 1;   /* rows per block */                                  \
+    k_ln_fwd<T, W, V, NV, WPR><<<(T_ + (int64_t)rpb - 1) / rpb, rpb * WPR * 32, 0, s>>>(      \
+        x, ldx, w, b, y, mean, rstd, T_, d, inv_d, eps);                                      \
+  } while (0)
+#define LN_W(NV)                                                                              \
+  do {                                                                                        \
+    if (wpr == 1) LN_GO(NV, 1);                                                               \
+    else if (wpr == 2) LN_GO(NV, 2);                                                          \
+    else if (wpr == 4) LN_GO(NV, 4);                                                          \
+    else if (wpr == 8) LN_GO(NV, 8);                                                          \
+    else if (wpr == 16) LN_GO(NV, 16);                                                        \
+    else LN_GO(NV, 32);                                                                       \
+  } while (0)
   if (nv > 8) k_ln_fwd_wide<T, W><<<T_, 1024, 0, s>>>(x, ldx, w, b, y, mean, rstd, d, eps);
-  else if (wpr <= 8 && nv > 4) LN_GO(8, 256);
-  else if (wpr <= 8 && nv > 2) LN_GO(4, 256);
-  else if (wpr <= 8) LN_GO(2, 256);
-  else if (nv > 4) LN_GO(8, 1024);
-  else if (nv > 2) LN_GO(4, 1024);
-  else LN_GO(2, 1024);
+  else if (nv > 4) LN_GO(8, 32);
+  else if (nv > 2) LN_W(4);
+  else LN_W(2);
+#undef LN_W
 #undef LN_GO
   MOE_CHECK_LAUNCH("layernorm_fwd");
   return MOE_OK;
@@ -433,40 +714,83 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
   return ln_fwd_v<T, W, 1>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
 }
 
-constexpr int LN_COLS = 8192;     // widest row of k_ln_bwd: 16 elements x 512 threads
+constexpr int LN_COLS = 8192;     // widest row of k_ln_bwd: 8 columns x 1024 threads
+constexpr int LN_PARTS = 148 * 4;    // most blocks of either kernel
 constexpr int LN_SLICES = 64;     // row slices of k_ln_bwd_cols
-constexpr int LN_SMS = 148;
-
-// Launch shape of k_ln_bwd: elements per thread, threads per row, rows per
-// block, blocks.
-struct LnShape {
-  int per, G, rpb, grid;
+// Launch shape of k_ln_bwd_ws; R = 0 where rows are not of 16-byte units or too
+// few to give every block a few stages.
+struct LnWs {
+  int R = 0, stages, ct, npk, grid;
+  size_t bytes;
 };
-LnShape ln_bwd_shape(int T_, int d) {
-  LnShape p;
-  p.per = d <= 4096 ? 8 : 16;
-  const int packs = (d + p.per - 1) / p.per;
-  p.G = (packs + 31) / 32 * 32;
-  p.rpb = p.G >= 256 ? 1 : 256 / p.G;
-  const int per_sm = p.G * p.rpb <= 256 ? 3 : 1;
-  const int64_t rows = ((int64_t)T_ + p.rpb - 1) / p.rpb;
-  p.grid = (int)(rows < LN_SMS * per_sm ? rows : LN_SMS * per_sm);
+LnWs ln_bwd_ws(int T_, int d, int es, bool add) {
+  LnWs p;
+  const int v = 16 / es;
+  if (d % v || d > LN_COLS) return p;
+  const int packs = d / v;
+  p.ct = 32;
+  while (p.ct < 32 * LN_CW && p.ct < packs) p.ct *= 2;
+  p.npk = (packs + p.ct - 1) / p.ct;
+  // two blocks per SM where the columns' registers allow it; stages of at
+  // least four rows (a row per warp) where three of them fit
+  const size_t rb = (size_t)d * es * (add ? 3 : 2), room = (p.npk == 1 ? 108 : 216) * 1024;
+  int r = 8;
+  while (r > 4 && 3 * r * rb > room) r /= 2;
+  while (r > 1 && 2 * r * rb > room) r /= 2;
+  p.stages = (int)std::min<size_t>(room / (r * rb), LN_STAGES);
+  p.grid = LN_SMS * (p.npk == 1 ? 2 : 1);
+  p.bytes = std::max((size_t)p.stages * r * rb, (size_t)8 * d);
+  if (p.stages < 2 || T_ < 4 * (int64_t)p.grid * r) return p;
+  p.R = r;
   return p;
+}
+
+template <class T, class W>
+int ln_bwd_ws_go(const LnWs& p, const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w,
+                 const float* mean, const float* rstd, const T* add, int64_t ldadd, int T_, int d,
+                 T* dx, float* part, cudaStream_t s) {
+  ProfScope _ps("layernorm_bwd", s);
+#define LN_GO(NPK)                                                                             \
+  do {                                                                                         \
+    if (cudaError_t e = smem_limit<k_ln_bwd_ws<T, W, NPK>>(216 * 1024))                        \
+      return cuda_fail(e, "layernorm smem attribute");                                         \
+    k_ln_bwd_ws<T, W, NPK><<<p.grid, LN_WS_THREADS, p.bytes, s>>>(                             \
+        dy, lddy, x, ldx, w, mean, rstd, add, ldadd, dx, part, T_, d, 1.0f / (float)d, p.R,    \
+        p.stages, p.ct, status_ptr());                                                         \
+  } while (0)
+  if (p.npk <= 1) LN_GO(1);
+  else if (p.npk <= 2) LN_GO(2);
+  else if (sizeof(T) == 2 || p.npk <= 4) LN_GO(4);
+  else if constexpr (sizeof(T) == 4) LN_GO(8);
+#undef LN_GO
+  MOE_CHECK_LAUNCH("layernorm_bwd");
+  return MOE_OK;
 }
 
 template <class T, class W, int V>
 int ln_bwd_v(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, const float* mean,
              const float* rstd, const T* add, int64_t ldadd, int T_, int d, T* dx, float* part,
-             cudaStream_t s) {
-  const LnShape p = ln_bwd_shape(T_, d);
-  const int threads = p.G * p.rpb;
+             int* nparts, cudaStream_t s) {
+  if constexpr (V * sizeof(T) == 16) {
+    const LnWs p = ln_bwd_ws(T_, d, sizeof(T), add != nullptr);
+    if (p.R) {
+      *nparts = p.grid;
+      return ln_bwd_ws_go<T, W>(p, dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T_, d, dx, part, s);
+    }
+  }
+  const int G = ((d + 7) / 8 + 31) / 32 * 32, groups = G >= 128 ? 1 : 128 / G, block = G * groups;
+  const size_t smem = groups > 1 ? (size_t)2 * d * sizeof(float) : 0;
+  const int64_t steps = ((int64_t)T_ + groups - 1) / groups;
+  const int grid = (int)std::min<int64_t>(steps, LN_SMS * (block <= 512 ? 512 / block : 1));
+  *nparts = grid;
   ProfScope _ps("layernorm_bwd", s);
-#define LN_GO(NV, MAXT, MINB)                                                                   \
-  k_ln_bwd<T, W, V, NV, MAXT, MINB><<<p.grid, threads, 0, s>>>(dy, lddy, x, ldx, w, mean, rstd, \
-                                                               add, ldadd, dx, part, T_, d, p.G)
-  if (p.per == 16) LN_GO(16 / V, 512, 1);
-  else if (threads > 256) LN_GO(8 / V, 512, 1);
-  else LN_GO(8 / V, 256, sizeof(T) == 2 ? 3 : 2);
+#define LN_GO(MAXT)                                                         \
+  k_ln_bwd<T, W, V, MAXT><<<grid, block, smem, s>>>(                        \
+      dy, lddy, x, ldx, w, mean, rstd, add, ldadd, dx, part, T_, d, 1.0f / (float)d, G)
+  if (block <= 128) LN_GO(128);
+  else if (block <= 256) LN_GO(256);
+  else if (block <= 512) LN_GO(512);
+  else LN_GO(1024);
 #undef LN_GO
   MOE_CHECK_LAUNCH("layernorm_bwd");
   return MOE_OK;
@@ -475,11 +799,12 @@ int ln_bwd_v(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, con
 template <class T, class W>
 int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
              const float* mean, const float* rstd, const void* add, int64_t ldadd, int T_, int d,
-             void* dx, float* part, cudaStream_t s) {
+             void* dx, float* part, int* nparts, cudaStream_t s) {
   const T *dyt = (const T*)dy, *xt = (const T*)x, *at = (const T*)add;
   const W* wt = (const W*)w;
   T* dxt = (T*)dx;
   if (d > LN_COLS) {
+    *nparts = LN_SLICES;
     if (part) {
       ProfScope _ps("layernorm_bwd_cols", s);
       const dim3 grid((d + 255) / 256, LN_SLICES);
@@ -493,7 +818,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
   }
   const int v = pick_pack<T, W>(d, {lddy, ldx, add ? ldadd : 0}, {dy, x, add, dx}, {w});
 #define LN_V(V) \
-  return ln_bwd_v<T, W, V>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, T_, d, dxt, part, s)
+  return ln_bwd_v<T, W, V>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, T_, d, dxt, part, nparts, s)
   if constexpr (sizeof(T) == 2) {
     if (v == 8) LN_V(8);
     if (v == 2) LN_V(2);
@@ -504,11 +829,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
 #undef LN_V
 }
 
-int ln_parts(int T_, int d) {
-  if (d > LN_COLS) return LN_SLICES;
-  const LnShape p = ln_bwd_shape(T_, d);
-  return p.grid * p.rpb;
-}
+int ln_parts(int T_, int d) { return d > LN_COLS ? LN_SLICES : std::min(T_, LN_PARTS); }
 
 }  // namespace
 
@@ -532,20 +853,29 @@ int launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ld
                          int T, int d, int dtype, int wdtype, void* dx, float* dweight,
                          float* dbias, float* part, cudaStream_t s) {
   if (dweight == nullptr && dbias == nullptr) part = nullptr;
-  int rc;
+  int rc, nparts = 0;
   if (dtype == MOE_BF16)
     rc = wdtype == MOE_BF16
-             ? ln_bwd_t<__nv_bfloat16, __nv_bfloat16>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, s)
-             : ln_bwd_t<__nv_bfloat16, float>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, s);
+             ? ln_bwd_t<__nv_bfloat16, __nv_bfloat16>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, &nparts, s)
+             : ln_bwd_t<__nv_bfloat16, float>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, &nparts, s);
   else
     rc = wdtype == MOE_BF16
-             ? ln_bwd_t<float, __nv_bfloat16>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, s)
-             : ln_bwd_t<float, float>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, s);
+             ? ln_bwd_t<float, __nv_bfloat16>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, &nparts, s)
+             : ln_bwd_t<float, float>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, &nparts, s);
   if (rc || part == nullptr) return rc;
+  // launched as a dependent: its blocks are ready when the last row is done
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = (unsigned)((2 * (int64_t)d + 31) / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   ProfScope _ps("layernorm_reduce", s);
-  k_ln_reduce<<<(unsigned)((2 * (int64_t)d + 31) / 32), dim3(32, 32), 0, s>>>(part, ln_parts(T, d), d,
-                                                                              dweight, dbias);
-  MOE_CHECK_LAUNCH("layernorm_reduce");
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, k_ln_reduce, (const float*)part, nparts, d, dweight, dbias))
+    return cuda_fail(e, "layernorm_reduce");
   return MOE_OK;
 }
 

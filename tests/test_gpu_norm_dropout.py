@@ -79,7 +79,8 @@ def check_ln(x, w, b, eps=1e-5, dy=None, add=None):
 
 SHAPES = [(1, 1), (1, 7168), (3, 2), (5, 31), (64, 33), (129, 128), (300, 250), (17, 1000), (37, 1037),
           (1000, 256), (450, 2048), (700, 1536), (40, 4096), (33, 4104), (20, 7168), (9, 8191),
-          (12, 8192), (3, 8200), (2, 12345), (2, 70000), (4000, 64)]
+          (12, 8192), (3, 8200), (2, 12345), (2, 70000), (4000, 64), (3001, 256), (2999, 1536), (1500, 2048),
+          (2500, 2056), (800, 4096), (700, 7168), (650, 8192), (620, 8184), (5000, 2048), (4800, 512), (9500, 128), (2600, 7168), (1300, 8192)]
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
