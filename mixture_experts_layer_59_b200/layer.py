@@ -1,5 +1,6 @@
-"""One MoE layer step (forward + backward) through the C ABI, with every
-buffer allocated once up front so that a step allocates nothing."""
+"""One MoE layer step, and one step of the transformer block's feed-forward half
+around it (forward + backward), through the C ABI, with every buffer allocated
+once up front so that a step allocates nothing."""
 from __future__ import annotations
 
 import torch
@@ -124,3 +125,82 @@ class MoELayerStep:
                                self.H, self.router_grad, out=self.grads, ws=self.ws_bwd,
                                stream=stream, gate_grad=gate_grad, logits=self.logits,
                                gate_mode=self.gate_mode)
+
+
+class MoEBlockStep:
+    """The feed-forward half of a transformer block around the layer:
+
+        n = layer_norm(x),  y = x + dropout(MoE(n) + FFN(n))
+
+    FFN is the shared expert, a dense gated feed-forward block of width
+    ``f_shared`` that every token passes.  bf16 activations and weights; the
+    norm's weight and bias are bf16 or fp32.
+
+    forward(): moe_layernorm_fwd -> MoELayerStep.forward -> moe_shared_ffn_fwd
+        (adds the routed experts' output in its epilogue) -> moe_dropout_fwd
+        (adds x)
+    backward(): moe_dropout_bwd -> MoELayerStep.backward -> moe_shared_ffn_bwd
+        (adds the routed experts' dx) -> moe_layernorm_bwd (adds dy, the
+        gradient that passes by)
+
+    ``moe`` is the MoELayerStep inside (routing results, expert gradients);
+    further keyword arguments are its own.
+    """
+
+    def __init__(self, T, d, f, E, k, f_shared, p=0.0, eps=1e-5, device="cuda", **layer):
+        dtype = torch.bfloat16
+        if layer.setdefault("dtype", dtype) != dtype:
+            raise ValueError("MoEBlockStep is bf16 only")
+        self.p, self.eps = p, eps
+        self.moe = MoELayerStep(T, d, f, E, k, device=device, **layer)
+        e = lambda *s, dt=dtype: torch.empty(*s, device=device, dtype=dt)  # noqa: E731
+        f32, u8, fs = torch.float32, torch.uint8, f_shared
+        self.n, self.mean, self.rstd = e(T, d), e(T, dt=f32), e(T, dt=f32)
+        self.Hs, self.m, self.y = e(T, 2 * fs), e(T, d), e(T, d)
+        self.ws_fwd = e(max(B.moe_shared_ffn_fwd_workspace_size(T, d, fs), 1), dt=u8)
+        self.ws_bwd = e(max(B.moe_shared_ffn_bwd_workspace_size(T, d, fs), 1), dt=u8)
+        self.ws_ln = e(max(B.moe_layernorm_bwd_workspace_size(T, d), 1), dt=u8)
+        self.dm = e(T, d)
+        self.ffn_grads = dict(dx=e(T, d), dw1=e(d, fs), dw3=e(d, fs), dw2=e(fs, d))
+        self.ln_grads = dict(dx=e(T, d), dweight=e(d, dt=f32), dbias=e(d, dt=f32))
+
+    def forward(self, x, ln, experts, shared, rng, stream=None, **route):
+        """ln: (weight, bias); experts: (w_gate, w1, w3, w2); shared: (w1, w3,
+        w2); rng: int64 [2] on the device, (seed, offset); route: what
+        MoELayerStep.forward takes besides."""
+        self._saved = (x, ln, shared, rng)
+        B.moe_layernorm_fwd(x, *ln, eps=self.eps, y=self.n, mean=self.mean, rstd=self.rstd,
+                            stream=stream)
+        out = self.moe.forward(self.n, *experts, stream=stream, **route)
+        B.moe_shared_ffn_fwd(self.n, *shared, addend=out, H=self.Hs, y=self.m, ws=self.ws_fwd,
+                             stream=stream)
+        return B.moe_dropout_fwd(self.m, self.p, rng, residual=x, out=self.y, stream=stream)
+
+    def backward(self, dy, stream=None):
+        """Returns dict dx, ln_weight, ln_bias, shared_w1, shared_w3, shared_w2 and
+        the experts' gradients under MoELayerStep's names (without its dx)."""
+        x, ln, shared, rng = self._saved
+        B.moe_dropout_bwd(dy, self.p, rng, dx=self.dm, stream=stream)
+        g = self.moe.backward(self.dm, stream=stream)
+        f = B.moe_shared_ffn_bwd(self.dm, self.n, *shared, self.Hs, addend=g["dx"],
+                                 out=self.ffn_grads, ws=self.ws_bwd, stream=stream)
+        n = B.moe_layernorm_bwd(f["dx"], x, ln[0], self.mean, self.rstd, addend=dy,
+                                out=self.ln_grads, ws=self.ws_ln, stream=stream)
+        return dict({k: v for k, v in g.items() if k != "dx"}, dx=n["dx"], ln_weight=n["dweight"],
+                    ln_bias=n["dbias"], shared_w1=f["dw1"], shared_w3=f["dw3"],
+                    shared_w2=f["dw2"])
+
+    def capture(self, x, ln, experts, shared, rng, dy, **route):
+        """One forward + backward step as a CUDA graph (as MoELayerStep.capture).
+        A replay reads rng's current values: change its offset between steps."""
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            self.forward(x, ln, experts, shared, rng, **route)
+            self.backward(dy)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+            self.forward(x, ln, experts, shared, rng, **route)
+            self.backward(dy)
+        return graph
