@@ -589,18 +589,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(o, name, shape, dtype, device):
+def _out(o, name, shape, like, dtype):
     t = o.get(name)
     if t is None:
-        t = o[name] = torch.empty(shape, device=device, dtype=dtype)
+        t = o[name] = like.new_empty(shape, dtype=dtype)
     else:
-        _arg(name, t, shape, dtype, device)
+        _arg(name, t, shape, dtype, like.device)
     return t.data_ptr()
 
 
-def _ws(ws, size, device):
+def _ws(ws, size, like):
     if ws is None:
-        return torch.empty(size if size > 0 else 1, device=device, dtype=torch.uint8)
+        return like.new_empty(size if size > 0 else 1, dtype=torch.uint8)
+    device = like.device
     if ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
         _bad(f"ws: expected a contiguous uint8 tensor on {device}")
     return ws
@@ -628,11 +629,11 @@ def moe_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rs
         with _there(x, stream):
             return moe_layernorm_fwd(x, weight, bias, eps, y, mean, rstd)
     if y is None:
-        y = torch.empty((T, d), device=dev, dtype=x.dtype)
+        y = x.new_empty((T, d))
     else:
         _arg("y", y, (T, d), x.dtype, dev)
     if mean is None:
-        mean, rstd = torch.empty(T, device=dev, dtype=_F32), torch.empty(T, device=dev, dtype=_F32)
+        mean, rstd = x.new_empty(T, dtype=_F32), x.new_empty(T, dtype=_F32)
     else:
         _arg("mean", mean, (T,), _F32, dev)
         _arg("rstd", rstd, (T,), _F32, dev)
@@ -664,9 +665,9 @@ def moe_layernorm_bwd(dy, x, weight, mean, rstd, addend=None, out=None, ws=None,
         with _there(x, stream):
             return moe_layernorm_bwd(dy, x, weight, mean, rstd, addend, out, ws)
     o = dict(out) if out else {}
-    dx = _out(o, "dx", (T, d), x.dtype, dev)
-    dw, db = _out(o, "dweight", (d,), _F32, dev), _out(o, "dbias", (d,), _F32, dev)
-    ws = _ws(ws, lib().moe_layernorm_bwd_workspace_size(T, d), dev)
+    dx = _out(o, "dx", (T, d), x, x.dtype)
+    dw, db = _out(o, "dweight", (d,), x, _F32), _out(o, "dbias", (d,), x, _F32)
+    ws = _ws(ws, lib().moe_layernorm_bwd_workspace_size(T, d), x)
     _check(lib().moe_layernorm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, _ptr(weight),
                                    mean.data_ptr(), rstd.data_ptr(), _ptr(addend), ldadd, T, d, dt,
                                    wdt, dx, dw, db, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
@@ -739,14 +740,14 @@ def moe_shared_ffn_fwd(x, w1, w3, w2, addend=None, H=None, y=None, save=True, ws
     if not save:
         H = None
     elif H is None:
-        H = torch.empty((T, 2 * f), device=dev, dtype=x.dtype)
+        H = x.new_empty((T, 2 * f))
     else:
         _arg("H", H, (T, 2 * f), x.dtype, dev)
     if y is None:
-        y = torch.empty((T, d), device=dev, dtype=x.dtype)
+        y = torch.empty_like(x)
     else:
         _arg("y", y, (T, d), x.dtype, dev)
-    ws = _ws(ws, lib().moe_shared_ffn_fwd_workspace_size(T, d, f, dt), dev)
+    ws = _ws(ws, lib().moe_shared_ffn_fwd_workspace_size(T, d, f, dt), x)
     _check(lib().moe_shared_ffn_fwd(x.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
                                     _ptr(addend), T, d, f, dt, _ptr(H), y.data_ptr(),
                                     ws.data_ptr(), ws.numel(), _raw_stream(dev)))
@@ -769,10 +770,10 @@ def moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend=None, out=None, ws=None, s
         with _there(x, stream):
             return moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend, out, ws)
     o = dict(out) if out else {}
-    dx = _out(o, "dx", (T, d), x.dtype, dev)
-    dw1, dw3 = _out(o, "dw1", (d, f), x.dtype, dev), _out(o, "dw3", (d, f), x.dtype, dev)
-    dw2 = _out(o, "dw2", (f, d), x.dtype, dev)
-    ws = _ws(ws, lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dt), dev)
+    dx = _out(o, "dx", (T, d), x, x.dtype)
+    dw1, dw3 = _out(o, "dw1", (d, f), x, x.dtype), _out(o, "dw3", (d, f), x, x.dtype)
+    dw2 = _out(o, "dw2", (f, d), x, x.dtype)
+    ws = _ws(ws, lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dt), x)
     _check(lib().moe_shared_ffn_bwd(dout.data_ptr(), x.data_ptr(), w1.data_ptr(), w3.data_ptr(),
                                     w2.data_ptr(), H.data_ptr(), _ptr(addend), T, d, f, dt, dx,
                                     dw1, dw3, dw2, ws.data_ptr(), ws.numel(), _raw_stream(dev)))

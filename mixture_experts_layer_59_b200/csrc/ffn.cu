@@ -15,6 +15,8 @@
 // is no row space: the tensor maps end at T, d and f, loads past them read
 // zeros and stores past them are clipped, so any T and any d, f that are
 // multiples of 8 (the 16-byte row strides TMA needs) work.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc_tile.cuh"
@@ -39,6 +41,7 @@ struct FfnArgs {
   float4* part;        // pairs: fp32 partials [pair][first or second segment][rank][PART4]
   int* count;          // pairs: arrivals [shared tile][rank], zero at the start
   int kbs, kbh;        // k-blocks per tile; DX: of them with dH1
+  int stages;          // split: stages of the pipeline in use
   int a4, b4;          // operand widths are multiples of 64: one box per stage
   int save_h;          // UP: write H
   const __nv_bfloat16* hin;     // DAP
@@ -155,18 +158,27 @@ __device__ __forceinline__ uint32_t part_off(int row, int chunk) {
   return (uint32_t)(row * BN * 4 + ((chunk ^ (row & 7)) << 4));
 }
 
-// Columns c .. c+7 of a row, summed over the cluster's partials in rank order.
+// Columns c .. c+7 of a row, summed over the cluster's partials in rank order;
+// the loads from all ranks are in flight together.
+constexpr int MAX_RANKS = 8;
 template <int BN>
 __device__ __forceinline__ void part_sum8(uint32_t base, int nranks, int row, int c, float (&v)[8]) {
+  float4 x[MAX_RANKS], y[MAX_RANKS];
+#pragma unroll
+  for (int r = 0; r < MAX_RANKS; ++r)
+    if (r < nranks) {
+      const uint32_t b = map_shared(base, r);
+      x[r] = ld_cluster_v4(b + part_off<BN>(row, c / 4));
+      y[r] = ld_cluster_v4(b + part_off<BN>(row, c / 4 + 1));
+    }
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  for (int r = 0; r < nranks; ++r) {
-    const uint32_t b = map_shared(base, r);
-    const float4 x = ld_cluster_v4(b + part_off<BN>(row, c / 4));
-    const float4 y = ld_cluster_v4(b + part_off<BN>(row, c / 4 + 1));
-    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-  }
+#pragma unroll
+  for (int r = 0; r < MAX_RANKS; ++r)
+    if (r < nranks) {
+      v[0] += x[r].x; v[1] += x[r].y; v[2] += x[r].z; v[3] += x[r].w;
+      v[4] += y[r].x; v[5] += y[r].y; v[6] += y[r].z; v[7] += y[r].w;
+    }
 }
 
 // Few rows: the CTAs of a cluster share one 128 x BN tile, each takes a slice
@@ -204,46 +216,63 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem_base = s_tmem;
-  grid_dependency_wait();      // the previous product's results
   grid_launch_dependents();
   const int nranks = (int)cluster_size(), rank = (int)cluster_rank();
   const FTile ti = f_tile<KIND, BN, BM>((int)blockIdx.x / nranks, a);
   const int kb_begin = (int)((int64_t)a.kbs * rank / nranks);
   const int kb_end = (int)((int64_t)a.kbs * (rank + 1) / nranks);
+  const int stages = a.stages;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0 && !a.dbg_no_load) {
-      int stage = 0;
-      uint32_t phase = 0;
-        for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (!bounded_wait(&empty_bar[stage], phase ^ 1, &s_abort, a.status, 1, a.wait_ns)) break;
-          uint8_t* sA = smem + stage * C::STAGE;
-          uint8_t* sB = sA + A_BYTES;
-          uint64_t* bar = &full_bar[stage];
-          mbar_arrive_expect_tx(bar, C::STAGE);
-          const int k0 = kb * BK;
-          if constexpr (KIND == F_UP) {
-            tma_load_2d(sA, &a.mA[0], bar, k0, ti.m0);
-            load_mn<BN / 128>(sB, &a.mB[0], bar, k0, ti.n0, a.b4);
-            load_mn<BN / 128>(sB + (BN / 128) * ATOM, &a.mB[1], bar, k0, ti.n0, a.b4);
-          } else if constexpr (KIND == F_DOWN) {
-            tma_load_2d(sA, &a.mA[0], bar, k0, ti.m0);
-            load_mn<BN / 64>(sB, &a.mB[0], bar, k0, ti.n0, a.b4);
-          } else if constexpr (KIND == F_DAP) {
-            tma_load_2d(sA, &a.mA[0], bar, k0, ti.m0);
-            tma_load_2d(sB, &a.mB[0], bar, k0, ti.n0);
-          } else if constexpr (KIND == F_DX) {
-            const int h = kb >= a.kbh;
-            const int kk = h ? k0 - a.kbh * BK : k0;
-            tma_load_2d(sA, &a.mA[h], bar, kk, ti.m0);
-            tma_load_2d(sB, &a.mB[h], bar, kk, ti.n0);
-          } else {
-            load_mn<BM / 64>(sA, &a.mA[ti.p], bar, k0, ti.m0, (a.a4 >> ti.p) & 1);
-            load_mn<BN / 64>(sB, &a.mB[ti.p], bar, k0, ti.n0, (a.b4 >> ti.p) & 1);
-          }
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+      auto load_a = [&](int stage, int kb) {
+        uint8_t* sA = smem + stage * C::STAGE;
+        uint64_t* bar = &full_bar[stage];
+        const int k0 = kb * BK;
+        if constexpr (KIND == F_DX) {
+          const int h = kb >= a.kbh;
+          tma_load_2d(sA, &a.mA[h], bar, h ? k0 - a.kbh * BK : k0, ti.m0);
+        } else if constexpr (KIND == F_DW) {
+          load_mn<BM / 64>(sA, &a.mA[ti.p], bar, k0, ti.m0, (a.a4 >> ti.p) & 1);
+        } else {
+          tma_load_2d(sA, &a.mA[0], bar, k0, ti.m0);
         }
+      };
+      auto load_b = [&](int stage, int kb) {
+        uint8_t* sB = smem + stage * C::STAGE + A_BYTES;
+        uint64_t* bar = &full_bar[stage];
+        const int k0 = kb * BK;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        if constexpr (KIND == F_UP) {
+          load_mn<BN / 128>(sB, &a.mB[0], bar, k0, ti.n0, a.b4);
+          load_mn<BN / 128>(sB + (BN / 128) * ATOM, &a.mB[1], bar, k0, ti.n0, a.b4);
+        } else if constexpr (KIND == F_DOWN) {
+          load_mn<BN / 64>(sB, &a.mB[0], bar, k0, ti.n0, a.b4);
+        } else if constexpr (KIND == F_DAP) {
+          tma_load_2d(sB, &a.mB[0], bar, k0, ti.n0);
+        } else if constexpr (KIND == F_DX) {
+          const int h = kb >= a.kbh;
+          tma_load_2d(sB, &a.mB[h], bar, h ? k0 - a.kbh * BK : k0, ti.n0);
+        } else {
+          load_mn<BN / 64>(sB, &a.mB[ti.p], bar, k0, ti.n0, (a.b4 >> ti.p) & 1);
+        }
+      };
+      // The weights do not come from the product before this one: the first
+      // stages' are fetched while it still runs.
+      constexpr bool EARLY = KIND != F_DW;
+      const int early = EARLY ? min(stages, kb_end - kb_begin) : 0;
+      for (int i = 0; i < early; ++i) load_b(i, kb_begin + i);
+      grid_dependency_wait();
+      for (int i = 0; i < early; ++i) load_a(i, kb_begin + i);
+      int stage = early == stages ? 0 : early;
+      uint32_t phase = early == stages ? 1 : 0;
+      for (int kb = kb_begin + early; kb < kb_end; ++kb) {
+        if (!bounded_wait(&empty_bar[stage], phase ^ 1, &s_abort, a.status, 1, a.wait_ns)) break;
+        load_b(stage, kb);
+        load_a(stage, kb);
+        if (++stage == stages) { stage = 0; phase ^= 1; }
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -251,22 +280,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
       constexpr uint32_t IDESC = idesc_bf16(BM, BN, FK<KIND>::A_MN, FK<KIND>::B_MN);
       int stage = 0;
       uint32_t phase = 0;
-        for (int kb = kb_begin; kb < kb_end; ++kb) {
-          if (!bounded_wait(&full_bar[stage], phase, &s_abort, a.status, 3, a.wait_ns)) break;
-          fence_after_sync();
-          const uint32_t sA = smem_u32(smem + stage * C::STAGE);
-          const uint32_t sB = sA + A_BYTES;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!bounded_wait(&full_bar[stage], phase, &s_abort, a.status, 3, a.wait_ns)) break;
+        fence_after_sync();
+        const uint32_t sA = smem_u32(smem + stage * C::STAGE);
+        const uint32_t sB = sA + A_BYTES;
 #pragma unroll
-          for (int ks = 0; ks < BK / 16; ++ks) {
-            const uint64_t ad = FK<KIND>::A_MN ? sdesc_sw128(sA + ks * 2048, ATOM, 1024)
-                                               : sdesc_sw128(sA + ks * 32, 16, 1024);
-            const uint64_t bd = FK<KIND>::B_MN ? sdesc_sw128(sB + ks * 2048, ATOM, 1024)
-                                               : sdesc_sw128(sB + ks * 32, 16, 1024);
-            umma_bf16(tmem_base, ad, bd, IDESC, kb > kb_begin || ks > 0);
-          }
-          umma_commit(&empty_bar[stage]);
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+        for (int ks = 0; ks < BK / 16; ++ks) {
+          const uint64_t ad = FK<KIND>::A_MN ? sdesc_sw128(sA + ks * 2048, ATOM, 1024)
+                                             : sdesc_sw128(sA + ks * 32, 16, 1024);
+          const uint64_t bd = FK<KIND>::B_MN ? sdesc_sw128(sB + ks * 2048, ATOM, 1024)
+                                             : sdesc_sw128(sB + ks * 32, 16, 1024);
+          umma_bf16(tmem_base, ad, bd, IDESC, kb > kb_begin || ks > 0);
         }
+        umma_commit(&empty_bar[stage]);
+        if (++stage == stages) { stage = 0; phase ^= 1; }
+      }
       umma_commit(&tfull_bar);
     }
   } else {
@@ -275,6 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
     const int half = (warp - 2) >> 2;            // which half of the tile's columns
     const int rloc = q * 32 + lane;              // row of the tile owned by this thread
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
+    grid_dependency_wait();   // before anything below reads or writes memory
     // this slice's partial, fp32, over the pipeline's stages: every copy into
     // them has landed and every MMA that reads them is done
     if (bounded_wait(&tfull_bar, 0, &s_abort, a.status, 4, a.wait_ns) &&
@@ -294,6 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
   }
 
   __syncwarp();
+  grid_dependency_wait();
   cluster_sync();            // every partial of the tile is in place
   {
     const int M = a.M[ti.p], N = a.N[ti.p];
@@ -875,9 +906,9 @@ const char* f_name(int kind) {
 }
 
 template <auto* KERNEL>
-int f_go(const FfnArgs& a, int kind, int grid, int block, int cluster, int smem, bool dependent,
-         cudaStream_t s) {
-  if (cudaError_t e = smem_limit<KERNEL>(smem)) return cuda_fail(e, "ffn smem attribute");
+int f_go(const FfnArgs& a, int kind, int grid, int block, int cluster, int smem, int most_smem,
+         bool dependent, cudaStream_t s) {
+  if (cudaError_t e = smem_limit<KERNEL>(most_smem)) return cuda_fail(e, "ffn smem attribute");
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -992,16 +1023,30 @@ int f_launch(FfnArgs& a, const FPlan& p, bool dependent, cudaStream_t s) {
   a.share = p.share;
   a.span = p.span;
   if (p.split) {
-    const int grid = p.tiles * p.cluster;
-    return p.bn == 256
-               ? f_go<k_ffn_split<KIND, 256>>(a, KIND, grid, THREADS, p.cluster, FCfg<256>::SMEM,
-                                              dependent, s)
-               : f_go<k_ffn_split<KIND, 128>>(a, KIND, grid, THREADS, p.cluster, FCfg<128>::SMEM,
-                                              dependent, s);
+    // Shared memory: the stages in use (all of a CTA's slice, where it fits),
+    // which then hold the partial of the rows that exist.  At least 448 bytes
+    // per TMEM column, so that the CTAs of an SM never ask for more than its
+    // 512 columns: a CTA that waited for columns could hold up its cluster.
+    const int rows32 = a.M[0] >= BM || KIND == F_DW ? BM : (a.M[0] + 31) / 32 * 32;
+    const int grid = p.tiles * p.cluster, slice = (a.kbs + p.cluster - 1) / p.cluster;
+    auto go = [&](auto cfg, auto launch) {
+      typedef decltype(cfg) C;
+      a.stages = std::min(slice, (int)C::STAGES);
+      return launch(std::max(std::max(a.stages * C::STAGE, rows32 * p.bn * 4), 448 * p.bn));
+    };
+    if (p.bn == 256)
+      return go(FCfg<256>{}, [&](int smem) {
+        return f_go<k_ffn_split<KIND, 256>>(a, KIND, grid, THREADS, p.cluster, smem,
+                                            FCfg<256>::SMEM, dependent, s);
+      });
+    return go(FCfg<128>{}, [&](int smem) {
+      return f_go<k_ffn_split<KIND, 128>>(a, KIND, grid, THREADS, p.cluster, smem, FCfg<128>::SMEM,
+                                          dependent, s);
+    });
   }
   const int pairs = p.share || p.whole > MAX_PAIRS ? MAX_PAIRS : p.whole;
-  return f_go<k_ffn_pair<KIND>>(a, KIND, 2 * pairs, PCfg<KIND>::BLOCK, 2, PCfg<KIND>::SMEM, dependent,
-                                s);
+  return f_go<k_ffn_pair<KIND>>(a, KIND, 2 * pairs, PCfg<KIND>::BLOCK, 2, PCfg<KIND>::SMEM,
+                                PCfg<KIND>::SMEM, dependent, s);
 }
 
 // An MN-major operand [rows, cols]: one box of `atoms` 64-column blocks where
