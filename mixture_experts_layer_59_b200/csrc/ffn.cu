@@ -42,6 +42,9 @@ struct FfnArgs {
   int* count;          // pairs: arrivals [shared tile][rank], zero at the start
   int kbs, kbh;        // k-blocks per tile; DX: of them with dH1
   int stages;          // split: stages of the pipeline in use
+  int a_rows;          // split: rows of A that a stage brings (the MMA's others are never read)
+  const uint8_t* next[2];   // split: weights of the next product (or null) and their bytes
+  int64_t next_bytes;
   int a4, b4;          // operand widths are multiples of 64: one box per stage
   int save_h;          // UP: write H
   const __nv_bfloat16* hin;     // DAP
@@ -140,14 +143,16 @@ __device__ __forceinline__ void load_mn_pair(uint8_t* dst, const CUtensorMap* m,
   }
 }
 
-// 8 bf16 results to p (16-byte aligned).
-__device__ __forceinline__ void st_bf16x8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint4 u;
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  memcpy(&u, h, 16);
-  *reinterpret_cast<uint4*>(p) = u;
+// 4 bf16 results to p (8-byte aligned); element k of 4 in a pair of words.
+__device__ __forceinline__ void st_bf16x4(__nv_bfloat16* p, const float (&v)[4]) {
+  __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+  uint2 u;
+  memcpy(&u, h, 8);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+__device__ __forceinline__ float bf16_of(const uint2& u, int k) {
+  const uint32_t w = k < 2 ? u.x : u.y;
+  return __uint_as_float((k & 1) ? (w & 0xffff0000u) : (w << 16));
 }
 
 // Split tiles: a tile's fp32 partial lies in each CTA's shared memory as rows
@@ -158,28 +163,7 @@ __device__ __forceinline__ uint32_t part_off(int row, int chunk) {
   return (uint32_t)(row * BN * 4 + ((chunk ^ (row & 7)) << 4));
 }
 
-// Columns c .. c+7 of a row, summed over the cluster's partials in rank order;
-// the loads from all ranks are in flight together.
 constexpr int MAX_RANKS = 8;
-template <int BN>
-__device__ __forceinline__ void part_sum8(uint32_t base, int nranks, int row, int c, float (&v)[8]) {
-  float4 x[MAX_RANKS], y[MAX_RANKS];
-#pragma unroll
-  for (int r = 0; r < MAX_RANKS; ++r)
-    if (r < nranks) {
-      const uint32_t b = map_shared(base, r);
-      x[r] = ld_cluster_v4(b + part_off<BN>(row, c / 4));
-      y[r] = ld_cluster_v4(b + part_off<BN>(row, c / 4 + 1));
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll
-  for (int r = 0; r < MAX_RANKS; ++r)
-    if (r < nranks) {
-      v[0] += x[r].x; v[1] += x[r].y; v[2] += x[r].z; v[3] += x[r].w;
-      v[4] += y[r].x; v[5] += y[r].y; v[6] += y[r].z; v[7] += y[r].w;
-    }
-}
 
 // Few rows: the CTAs of a cluster share one 128 x BN tile, each takes a slice
 // of its k-blocks, and the partial sums meet in distributed shared memory.
@@ -207,6 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
     fence_mbar_init();
     prefetch_tmap(&a.mA[0]);
     prefetch_tmap(&a.mB[0]);
+    if (KIND == F_UP || KIND == F_DX) prefetch_tmap(&a.mB[1]);
   }
   if (warp == 1) {
     tmem_alloc(&s_tmem, C::TMEM_COLS);
@@ -243,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
         uint8_t* sB = smem + stage * C::STAGE + A_BYTES;
         uint64_t* bar = &full_bar[stage];
         const int k0 = kb * BK;
-        mbar_arrive_expect_tx(bar, C::STAGE);
+        mbar_arrive_expect_tx(bar, C::B_BYTES + a.a_rows * BK * 2);
         if constexpr (KIND == F_UP) {
           load_mn<BN / 128>(sB, &a.mB[0], bar, k0, ti.n0, a.b4);
           load_mn<BN / 128>(sB + (BN / 128) * ATOM, &a.mB[1], bar, k0, ti.n0, a.b4);
@@ -272,6 +257,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
         load_b(stage, kb);
         load_a(stage, kb);
         if (++stage == stages) { stage = 0; phase ^= 1; }
+      }
+      // the next product's weights on their way to L2 while this one's sums meet
+      if constexpr (KIND == F_UP || KIND == F_DAP) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (a.next[i] != nullptr)
+            for (int64_t o = (int64_t)blockIdx.x * 16384; o < a.next_bytes;
+                 o += (int64_t)gridDim.x * 16384)
+              l2_prefetch(a.next[i] + o, (uint32_t)min((int64_t)16384, a.next_bytes - o));
       }
     }
   } else if (warp == 1) {
@@ -327,56 +321,100 @@ __global__ void __launch_bounds__(THREADS, 1) k_ffn_split(const __grid_constant_
   grid_dependency_wait();
   cluster_sync();            // every partial of the tile is in place
   {
+    // Each thread takes 4-column units of the rows (16 bytes of a partial: a
+    // warp reads whole rows of banks), NI at a time, so that their loads from
+    // all ranks are in flight together.  The sums run in rank order.
     const int M = a.M[ti.p], N = a.N[ti.p];
     const int rows = min(BM, M - ti.m0);
-    constexpr int UNITS = (KIND == F_UP ? BN / 2 : BN) / 8;   // 8-column units of a row
+    constexpr int UNITS = (KIND == F_UP ? BN / 2 : BN) / 4;   // of a row
+    constexpr int SUMS = KIND == F_UP ? 2 : 1, NI = KIND == F_UP ? 2 : 4;
     const uint32_t base = smem_u32(smem);
-    for (int i = rank * THREADS + threadIdx.x; i < rows * UNITS; i += nranks * THREADS) {
-      const int rl = i / UNITS, c = (i % UNITS) * 8, col = ti.n0 + c;
-      if (col >= N) continue;
-      const size_t row = (size_t)(ti.m0 + rl);
-      float v[8];
-      if constexpr (KIND == F_UP) {
-        float h3[8];
-        part_sum8<BN>(base, nranks, rl, c, v);
-        part_sum8<BN>(base, nranks, rl, BN / 2 + c, h3);
-        if (a.save_h) {
-          st_bf16x8(a.out[0] + row * a.ldo[0] + col, v);
-          st_bf16x8(a.out[1] + row * a.ldo[1] + col, h3);
+    const int step = nranks * THREADS;
+    const bool add = (KIND == F_DOWN || KIND == F_DX) && a.addend != nullptr;
+    for (int i0 = rank * THREADS + threadIdx.x; i0 < rows * UNITS; i0 += NI * step) {
+      float v[NI][SUMS][4];
+      uint2 p1[NI], p3[KIND == F_DAP ? NI : 1];
+      int rl[NI], c[NI];
+      bool in[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int i = i0 + j * step;
+        rl[j] = i / UNITS;
+        c[j] = (i % UNITS) * 4;
+        in[j] = i < rows * UNITS && ti.n0 + c[j] < N;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[j][0][k] = v[j][SUMS - 1][k] = 0.f;
+        if (!in[j]) continue;
+        const size_t row = (size_t)(ti.m0 + rl[j]);
+        const int col = ti.n0 + c[j];
+        if constexpr (KIND == F_DAP) {
+          const __nv_bfloat16* rp = a.hin + row * 2 * a.f + col;
+          p1[j] = *reinterpret_cast<const uint2*>(rp);
+          p3[j] = *reinterpret_cast<const uint2*>(rp + a.f);
+        } else if (add) {
+          p1[j] = *reinterpret_cast<const uint2*>(a.addend + row * N + col);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < MAX_RANKS; ++r) {
+        if (r >= nranks) continue;
+        const uint32_t b = map_shared(base, r);
+        float4 x[NI][SUMS];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          if (!in[j]) continue;
+#pragma unroll
+          for (int m = 0; m < SUMS; ++m)
+            x[j][m] = ld_cluster_v4(b + part_off<BN>(rl[j], (c[j] + m * (BN / 2)) / 4));
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * sigmoid_ftz(v[k]) * h3[k];
-        st_bf16x8(a.out[2] + row * a.ldo[2] + col, v);
-      } else if constexpr (KIND == F_DAP) {
-        uint4 p1[4], p3[4];
-        const __nv_bfloat16* rp = a.hin + row * 2 * a.f + col;
-        p1[0] = *reinterpret_cast<const uint4*>(rp);
-        p3[0] = *reinterpret_cast<const uint4*>(rp + a.f);
-        part_sum8<BN>(base, nranks, rl, c, v);
-        float d3[8], av[8];
+        for (int j = 0; j < NI; ++j) {
+          if (!in[j]) continue;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          swiglu_bwd(v[k], bf16_lane(p1, k), bf16_lane(p3, k), v[k], d3[k], av[k]);
+          for (int m = 0; m < SUMS; ++m) {
+            v[j][m][0] += x[j][m].x;
+            v[j][m][1] += x[j][m].y;
+            v[j][m][2] += x[j][m].z;
+            v[j][m][3] += x[j][m].w;
+          }
         }
-        st_bf16x8(a.out[0] + row * a.ldo[0] + col, v);
-        st_bf16x8(a.out[1] + row * a.ldo[1] + col, d3);
-        st_bf16x8(a.out[2] + row * a.ldo[2] + col, av);
-      } else {
-        uint4 p1[4];
-        const bool add = (KIND == F_DOWN || KIND == F_DX) && a.addend != nullptr;
-        if (add) p1[0] = *reinterpret_cast<const uint4*>(a.addend + row * N + col);
-        part_sum8<BN>(base, nranks, rl, c, v);
-        if (add) {
+      }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] += bf16_lane(p1, k);
+      for (int j = 0; j < NI; ++j) {
+        if (!in[j]) continue;
+        const size_t row = (size_t)(ti.m0 + rl[j]);
+        const int col = ti.n0 + c[j];
+        float(&t)[4] = v[j][0];
+        if constexpr (KIND == F_UP) {
+          float(&h3)[4] = v[j][SUMS - 1];
+          if (a.save_h) {
+            st_bf16x4(a.out[0] + row * a.ldo[0] + col, t);
+            st_bf16x4(a.out[1] + row * a.ldo[1] + col, h3);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = t[k] * sigmoid_ftz(t[k]) * h3[k];
+          st_bf16x4(a.out[2] + row * a.ldo[2] + col, t);
+        } else if constexpr (KIND == F_DAP) {
+          float d3[4], av[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            swiglu_bwd(t[k], bf16_of(p1[j], k), bf16_of(p3[j], k), t[k], d3[k], av[k]);
+          st_bf16x4(a.out[0] + row * a.ldo[0] + col, t);
+          st_bf16x4(a.out[1] + row * a.ldo[1] + col, d3);
+          st_bf16x4(a.out[2] + row * a.ldo[2] + col, av);
+        } else {
+          if (add) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] += bf16_of(p1[j], k);
+          }
+          const int o = KIND == F_DW ? ti.p : 0;
+          st_bf16x4(a.out[o] + row * a.ldo[o] + col, t);
         }
-        const int o = KIND == F_DW ? ti.p : 0;
-        st_bf16x8(a.out[o] + row * a.ldo[o] + col, v);
       }
     }
   }
   __syncwarp();
-  cluster_sync();            // no CTA leaves while its partial is still read
+  cluster_sync_relaxed();    // no CTA leaves while its partial is still read
   if (s_abort) {   // aborted: let copies and MMAs in flight land
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
@@ -953,6 +991,9 @@ int count_tiles(int kind, int d, int f, int T, int rows, int cols) {
   }
 }
 
+// Rows of A's boxes: what exists, in the 8-row units of the swizzle.
+int a_box_rows(int T) { return T >= BM ? BM : (T + 7) / 8 * 8; }
+
 FPlan f_plan(int kind, int T, int d, int f) {
   FPlan p = {};
   const int kd = (d + BK - 1) / BK, kf = (f + BK - 1) / BK, kt = (T + BK - 1) / BK;
@@ -985,20 +1026,22 @@ FPlan f_plan(int kind, int T, int d, int f) {
     }
     if (2 * rem > MAX_PAIRS) share((rem * kbs + MAX_PAIRS - 1) / MAX_PAIRS, kbs, 3);
   }
-  // Few tiles: clusters of at most 8 along K, all resident at once.
+  // Few tiles: clusters of at most 8 along K, all resident at once; the sums'
+  // way between SMs costs them a start and a clock per 16 bytes (measured 18
+  // and 13 per clock: 96 rows, 4 ranks, 128 and 256 columns).
+  const int rows = kind == F_DW ? BM : a_box_rows(T);
   for (int bn = 256; bn >= 128; bn /= 2) {
     const int tiles = count_tiles(kind, d, f, T, BM, bn);
-    if (tiles > 148) continue;
-    int c = 8;
-    while (c > 1 && (tiles * c > resident(c) || kbs < c)) --c;
-    const int64_t t = (int64_t)((kbs + c - 1) / c) * (256 + 2 * bn);
-    if (t < best) {
-      best = t;
-      p.split = true;
-      p.bn = bn;
-      p.cluster = c;
-      p.tiles = tiles;
-      p.whole = p.share = 0;
+    for (int c = 1; c <= MAX_RANKS && c <= kbs && tiles * c <= resident(c); ++c) {
+      const int64_t t = (int64_t)((kbs + c - 1) / c) * 2 * (rows + bn) + (c > 1 ? 1500 + rows * bn / 4 : 0);
+      if (t < best) {
+        best = t;
+        p.split = true;
+        p.bn = bn;
+        p.cluster = c;
+        p.tiles = tiles;
+        p.whole = p.share = 0;
+      }
     }
   }
   return p;
@@ -1027,7 +1070,8 @@ int f_launch(FfnArgs& a, const FPlan& p, bool dependent, cudaStream_t s) {
     // which then hold the partial of the rows that exist.  At least 448 bytes
     // per TMEM column, so that the CTAs of an SM never ask for more than its
     // 512 columns: a CTA that waited for columns could hold up its cluster.
-    const int rows32 = a.M[0] >= BM || KIND == F_DW ? BM : (a.M[0] + 31) / 32 * 32;
+    const int rows32 = KIND == F_DW ? BM : (a_box_rows(a.T) + 31) / 32 * 32;
+    a.a_rows = KIND == F_DW ? BM : a_box_rows(a.T);
     const int grid = p.tiles * p.cluster, slice = (a.kbs + p.cluster - 1) / p.cluster;
     auto go = [&](auto cfg, auto launch) {
       typedef decltype(cfg) C;
@@ -1114,6 +1158,8 @@ struct FCall {
     return a;
   }
   bool pairs(int kind) const { return !z.plan[kind].split; }
+  // Rows of A that one CTA loads per stage.
+  int a_rows(int kind) const { return z.plan[kind].split ? a_box_rows(T) : BM; }
   // Columns of B that one CTA loads per stage.
   int b_cols(int kind) const {
     const FPlan& p = z.plan[kind];
@@ -1152,13 +1198,15 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     a.save_h = H != nullptr;
     __nv_bfloat16* h = (__nv_bfloat16*)H;
     const int atoms = call.b_cols(F_UP) / 64;
-    if ((rc = make_map_2d(&a.mA[0], p.x, d, T, 64, BM))) return rc;
+    if ((rc = make_map_2d(&a.mA[0], p.x, d, T, 64, call.a_rows(F_UP)))) return rc;
     if ((rc = map_mn(&a.mB[0], p.w1, f, d, f, atoms, &b4))) return rc;
     if ((rc = map_mn(&a.mB[1], p.w3, f, d, f, atoms, &b4))) return rc;
     a.b4 = b4;
     set_out(a, 0, h, 2 * f);
     set_out(a, 1, H ? h + f : nullptr, 2 * f);
     set_out(a, 2, act, f);
+    a.next[0] = (const uint8_t*)p.w2;
+    a.next_bytes = (int64_t)d * f * 2;
     if ((rc = call.go<F_UP>(a))) return rc;
   }
   {  // DOWN
@@ -1166,7 +1214,7 @@ int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, 
     a.M[0] = T; a.N[0] = d;
     a.kbs = (f + BK - 1) / BK;
     a.addend = (const __nv_bfloat16*)addend;
-    if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, BM))) return rc;
+    if ((rc = make_map_2d(&a.mA[0], act, f, T, 64, call.a_rows(F_DOWN)))) return rc;
     if ((rc = map_mn(&a.mB[0], p.w2, d, f, d, call.b_cols(F_DOWN) / 64, &b4))) return rc;
     a.b4 = b4;
     set_out(a, 0, y, d);
@@ -1191,11 +1239,14 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.M[0] = T; a.N[0] = f;
     a.kbs = (d + BK - 1) / BK;
     a.hin = (const __nv_bfloat16*)H;
-    if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, BM))) return rc;
+    if ((rc = make_map_2d(&a.mA[0], dout, d, T, 64, call.a_rows(F_DAP)))) return rc;
     if ((rc = make_map_2d(&a.mB[0], p.w2, d, f, 64, call.b_cols(F_DAP)))) return rc;
     set_out(a, 0, dh, 2 * f);
     set_out(a, 1, dh + f, 2 * f);
     set_out(a, 2, act, f);
+    a.next[0] = (const uint8_t*)p.w1;
+    a.next[1] = (const uint8_t*)p.w3;
+    a.next_bytes = (int64_t)d * f * 2;
     if ((rc = call.go<F_DAP>(a))) return rc;
   }
   {  // DX
@@ -1205,7 +1256,9 @@ int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* adde
     a.kbs = 2 * a.kbh;
     a.addend = (const __nv_bfloat16*)addend;
     for (int h = 0; h < 2; ++h) {
-      if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B, 2 * f))) return rc;
+      if ((rc = make_map_2d(&a.mA[h], dh + h * f, f, T, 64, call.a_rows(F_DX), CU_TENSOR_MAP_SWIZZLE_128B,
+                            2 * f)))
+        return rc;
       if ((rc = make_map_2d(&a.mB[h], h ? p.w3 : p.w1, f, d, 64, call.b_cols(F_DX)))) return rc;
     }
     set_out(a, 0, dx, d);
