@@ -225,6 +225,124 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
   }
 }
 
+// Many rows that do not start at 16-byte units, x and y alike.  Each row is
+// walked in the 16-byte units that hold it: unit j holds columns V j - o ..,
+// o the row's offset in its first unit; columns outside the row count as
+// nothing, and whole units leave as one store.  The columns of a thread thus
+// move from row to row, so w and b lie in shared memory as fp32, skewed by one
+// word in 32 (column c at c + c / 32), which spreads a warp's reads of every
+// V-th column over the banks.  Persistent blocks of 8 warps, gw to a row.
+// 32000 x 1037 bf16 in XX us; by single elements 129.
+__device__ __forceinline__ int ln_skew(int c) { return c + (c >> 5); }
+
+template <class T, class W, int NV>
+__global__ void __launch_bounds__(256)
+k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
+               float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float inv_d,
+               float eps, int gw) {
+  extern __shared__ float params[];              // w, then b
+  __shared__ float red[2][2][8];
+  constexpr int V = 16 / (int)sizeof(T), HV = V / 2;
+  typedef Vals<T, V, 1> P;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp / gw, groups = 8 / gw, lin = (warp % gw) * 32 + lane, G = gw * 32;
+  float *sw = params, *sb = params + ln_skew(d) + 1;
+  for (int c = threadIdx.x; c < d; c += 256) {
+    if (w) sw[ln_skew(c)] = to_f(w[c]);
+    if (b) sb[ln_skew(c)] = to_f(b[c]);
+  }
+  __syncthreads();
+  auto sum = [&](float v, float* r) {            // over the row's warps
+    v = warp_sum(v);
+    if (gw == 1) return v;
+    if (lane == 0) r[warp] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(G) : "memory");
+    v = 0.f;
+    for (int i = 0; i < gw; ++i) v += r[grp * gw + i];
+    return v;
+  };
+  int odd = 0;
+  const int64_t rstep = (int64_t)gridDim.x * groups;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < T_; row += rstep, odd ^= 1) {
+    const T* xr = x + row * ldx;
+    const int o = (int)((reinterpret_cast<uintptr_t>(xr) & 15u) / sizeof(T));
+    const T* xa = xr - o;                        // the row's first unit
+    T* ya = y + row * d - o;
+    P raw[NV];
+    F2 v[NV * HV], acc = f2(0.f, 0.f);
+    // column of element k of unit i: inside the row?
+    auto in = [&](int i, int k) { return (unsigned)((lin + i * G) * V - o + k) < (unsigned)d; };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) raw[i].load(xa, (lin + i * G) * V, 0, o + d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool whole = in(i, 0) && in(i, V - 1);
+#pragma unroll
+      for (int j = 0; j < HV; ++j) {
+        F2 e = raw[i].pair(j);
+        if (!whole) {
+          const float2 t = f2_get(e);
+          e = f2(in(i, 2 * j) ? t.x : 0.f, in(i, 2 * j + 1) ? t.y : 0.f);
+        }
+        v[i * HV + j] = e;
+        acc = f2_add(acc, e);
+      }
+    }
+    const float2 a1 = f2_get(acc);
+    const float mu = sum(a1.x + a1.y, red[odd][0]) * inv_d;
+    const F2 nmu = f2(-mu, -mu);
+    acc = f2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool whole = in(i, 0) && in(i, V - 1);
+#pragma unroll
+      for (int j = 0; j < HV; ++j) {
+        F2 e = f2_add(v[i * HV + j], nmu);
+        if (!whole) {
+          const float2 t = f2_get(e);
+          e = f2(in(i, 2 * j) ? t.x : 0.f, in(i, 2 * j + 1) ? t.y : 0.f);
+        }
+        v[i * HV + j] = e;
+        acc = f2_fma(e, e, acc);
+      }
+    }
+    const float2 a2 = f2_get(acc);
+    const float rs = rsqrtf(sum(a2.x + a2.y, red[odd][1]) * inv_d + eps);
+    const F2 rs2 = f2(rs, rs);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lin + i * G) * V - o;
+      if (in(i, 0) && in(i, V - 1)) {
+        P out;
+#pragma unroll
+        for (int j = 0; j < HV; ++j) {
+          const int s0 = ln_skew(c + 2 * j), s1 = ln_skew(c + 2 * j + 1);
+          F2 e = f2_mul(v[i * HV + j], rs2);
+          if (w) e = f2_mul(e, f2(sw[s0], sw[s1]));
+          if (b) e = f2_add(e, f2(sb[s0], sb[s1]));
+          out.set_pair(j, e);
+        }
+        out.store(ya, (lin + i * G) * V, 0, o + d);
+      } else {
+        // a unit that the row shares with its neighbour, or none of it
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (in(i, k)) {
+            const float2 t = f2_get(v[i * HV + k / 2]);
+            float e = (k & 1 ? t.y : t.x) * rs;
+            if (w) e *= sw[ln_skew(c + k)];
+            if (b) e += sb[ln_skew(c + k)];
+            ya[(lin + i * G) * V + k] = from_f<T>(e);
+          }
+      }
+    }
+    if (lin == 0 && mean) {
+      mean[row] = mu;
+      rstd[row] = rs;
+    }
+  }
+}
+
 // Rows wider than the registers of a block: three passes over the row, the
 // second and third from the caches.
 template <class T, class W>
@@ -372,21 +490,27 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
   }
 }
 
-// Many rows of 16-byte units.  The same sums in three roles that never meet at
-// a barrier of the block, so that the loads, the rows' sums and the columns'
-// sums of different rows overlap: one thread brings stages of R rows by bulk
-// copies; four warps take each row's two sums over its columns; eight warps,
-// a thread to the same columns of all rows, take rows to dx and to the column
-// sums in their registers.  (The kernel above, whose warps all wait for each
-// row's sums, 86 us at 32768 x 1536 bf16 with an addend; with all 8 warps
-// first at the rows' sums, then at the columns, 87; this one 74 and 4 for the
-// partial rows' sums: 5.4 TB/s; a plain sum of two such tensors runs at 6.5.)
-constexpr int LN_CW = 8, LN_SW = 4;              // column warps, row-sum warps
-constexpr int LN_WS_THREADS = 32 * (LN_CW + LN_SW + 1);
+// Many rows.  The same sums in three roles that never meet at a barrier of the
+// block, so that the loads, the rows' sums and the columns' sums of different
+// rows overlap: one thread brings stages of R rows by bulk copies; a few warps
+// take each row's two sums over its columns; CW warps, a thread to the same E
+// columns of all rows, take rows to dx and to the column sums in their
+// registers.  (The kernel above, whose warps all wait for each row's sums, 86
+// us at 32768 x 1536 bf16 with an addend; with all 8 warps first at the rows'
+// sums, then at the columns, 87; this one 74 and 4 for the partial rows' sums:
+// 5.4 TB/s; a plain sum of two such tensors runs at 6.5.)
+// Rows that do not start and end at 16-byte units (V = 1) come with the bytes
+// around them (never another 16-byte unit than one that holds a byte of the
+// row) and are read from shared memory element by element, neighbouring
+// threads neighbouring columns.
 constexpr int LN_STAGES = 6;                     // at most
+// Row-sum warps: with 16 column warps three, so that 20 warps leave each
+// thread 96 registers.
+constexpr int ln_sum_warps(int cw) { return cw == 16 ? 3 : 4; }
+constexpr int ln_ws_threads(int cw) { return 32 * (cw + ln_sum_warps(cw) + 1); }
 
-template <class T, class W, int NPK>   // NPK: 16-byte packs of a row per column thread
-__global__ void __launch_bounds__(LN_WS_THREADS, NPK == 1 ? 2 : 1)
+template <class T, class W, int V, int E, int CW>
+__global__ void __launch_bounds__(ln_ws_threads(CW), CW == 8 ? 2 : 1)
 k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
             const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
             int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, float inv_d, int R,
@@ -396,19 +520,22 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
   // per row of a stage, as pairs of the same value: -mean, rstd, -s1 / d, -s2 / d
   __shared__ __align__(16) F2 stat[LN_STAGES][8][4];
   __shared__ volatile int s_abort;
-  constexpr int V = 16 / (int)sizeof(T), HV = V / 2;
-  typedef Vals<T, V, 1> P;
+  constexpr int SW = ln_sum_warps(CW);
+  constexpr int PG = V == 1 ? 2 : 1;             // packs at a time: a pair at least
+  typedef Vals<T, V, PG> P;
+  constexpr int NG = E / (V * PG), GP = P::NP;   // groups of packs per thread, pairs in one
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rb = (uint32_t)d * sizeof(T);
+  const uint32_t slot = V == 1 ? (rb + 15) / 16 * 16 + 16 : rb;   // a row's bytes in a stage
   const int na = add ? 3 : 2;
-  const uint32_t stage_bytes = (uint32_t)(na * R) * rb;
+  const uint32_t stage_bytes = (uint32_t)(na * R) * slot;
   const int64_t tiles = ((int64_t)T_ + R - 1) / R;
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < LN_STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&ready[i], LN_SW);
-      mbar_init(&empty[i], LN_CW);
+      mbar_init(&ready[i], SW);
+      mbar_init(&empty[i], CW);
     }
     fence_mbar_init();
   }
@@ -419,48 +546,66 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
     if (++st == stages) { st = 0; phase ^= 1; }
   };
   auto rows_of = [&](int64_t t) { return (int)(T_ - t * R < R ? T_ - t * R : R); };
-  if (warp == LN_CW + LN_SW) {
+  // where row r of array `arr` of the current stage begins (its source: p)
+  auto in_stage = [&](int arr, int r, const T* p) {
+    const uint32_t off = V == 1 ? (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u : 0u;
+    return reinterpret_cast<const T*>(smem + (size_t)st * stage_bytes + (size_t)(arr * R + r) * slot + off);
+  };
+  if (warp == CW + SW) {
     // ------------------------------------------------------------ loads
     if (lane == 0) {
+      auto bytes_of = [&](const T* p) {
+        return V == 1 ? (((uint32_t)reinterpret_cast<uintptr_t>(p) & 15u) + rb + 15) / 16 * 16 : rb;
+      };
+      auto bring = [&](int arr, int r, const T* p) {
+        bulk_load(smem + (size_t)st * stage_bytes + (size_t)(arr * R + r) * slot,
+                  reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15),
+                  bytes_of(p), &full[st]);
+      };
       for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
         if (!bounded_wait(&empty[st], phase ^ 1, &s_abort, status, 6, WAIT_LIMIT_NS)) break;
         const int rows = rows_of(t);
-        mbar_arrive_expect_tx(&full[st], (uint32_t)(na * rows) * rb);
-        uint8_t* base = smem + (size_t)st * stage_bytes;
+        uint32_t bytes = 0;
         for (int r = 0; r < rows; ++r) {
           const int64_t row = t * R + r;
-          bulk_load(base + (size_t)r * rb, x + row * ldx, rb, &full[st]);
-          bulk_load(base + (size_t)(R + r) * rb, dy + row * lddy, rb, &full[st]);
-          if (add) bulk_load(base + (size_t)(2 * R + r) * rb, add + row * ldadd, rb, &full[st]);
+          bytes += bytes_of(x + row * ldx) + bytes_of(dy + row * lddy);
+          if (add) bytes += bytes_of(add + row * ldadd);
+        }
+        mbar_arrive_expect_tx(&full[st], bytes);
+        for (int r = 0; r < rows; ++r) {
+          const int64_t row = t * R + r;
+          bring(0, r, x + row * ldx);
+          bring(1, r, dy + row * lddy);
+          if (add) bring(2, r, add + row * ldadd);
         }
       }
     }
-  } else if (warp >= LN_CW) {
+  } else if (warp >= CW) {
     // ------------------------------------------------------------ the rows' sums
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
       const int rows = rows_of(t);
-      const uint8_t* base = smem + (size_t)st * stage_bytes;
-      const int64_t r0 = t * R + warp - LN_CW;   // this warp's first row: its statistics early
-      const bool any = warp - LN_CW < rows;
+      const int64_t r0 = t * R + warp - CW;   // this warp's first row: its statistics early
+      const bool any = warp - CW < rows;
       const float mu0 = any ? mean[r0] : 0.f, rs0 = any ? rstd[r0] : 0.f;
       // a warp without a row waits too: it must not run ahead of the stage
       bounded_wait(&full[st], phase, &s_abort, status, 7, WAIT_LIMIT_NS);
-      for (int r = warp - LN_CW; r < rows; r += LN_SW) {
-        const bool first = r == warp - LN_CW;
-        const float mu = first ? mu0 : mean[t * R + r], rs = first ? rs0 : rstd[t * R + r];
+      for (int r = warp - CW; r < rows; r += SW) {
+        const bool first = r == warp - CW;
+        const int64_t row = t * R + r;
+        const float mu = first ? mu0 : mean[row], rs = first ? rs0 : rstd[row];
         const F2 nmu = f2(-mu, -mu);
-        const T* xr = reinterpret_cast<const T*>(base + (size_t)r * rb);
-        const T* dr = reinterpret_cast<const T*>(base + (size_t)(R + r) * rb);
+        const T *xr = in_stage(0, r, x + row * ldx), *dr = in_stage(1, r, dy + row * lddy);
         F2 t1 = f2(0.f, 0.f), t2 = t1;
+        // columns past the row read zero and have dy = 0
 #pragma unroll 4
-        for (int c = lane * V; c < d; c += 32 * V) {
+        for (int c = lane * V; c < d; c += 32 * V * PG) {
           P px, pd;
-          Vals<W, V, 1> pw;
-          px.load(xr, c, 0, d);
-          pd.load(dr, c, 0, d);
-          if (w) pw.load(w, c, 0, d);
+          Vals<W, V, PG> pw;
+          px.load(xr, c, 32 * V, d);
+          pd.load(dr, c, 32 * V, d);
+          if (w) pw.load(w, c, 32 * V, d);
 #pragma unroll
-          for (int j = 0; j < HV; ++j) {
+          for (int j = 0; j < GP; ++j) {
             const F2 g = w ? f2_mul(pd.pair(j), pw.pair(j)) : pd.pair(j);
             t1 = f2_add(t1, g);
             t2 = f2_fma(g, f2_add(px.pair(j), nmu), t2);   // rstd times this: sum g xh
@@ -480,42 +625,41 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
     }
   } else {
     // ------------------------------------------------------------ dx and the columns' sums
-    // ct threads side by side cover a row's packs; the others take other rows
-    const int sg = threadIdx.x / ct, c0 = (threadIdx.x % ct) * V, cstep = ct * V;
-    const int nsg = 32 * LN_CW / ct;
-    F2 aw[NPK * HV], ab[NPK * HV], wv[NPK * HV];
+    // ct threads side by side cover a row; the next ct take the next row
+    const int nsg = 32 * CW / ct, sg = threadIdx.x / ct;
+    const int c0 = (threadIdx.x % ct) * V, cstep = ct * V;
+    F2 aw[NG * GP], ab[NG * GP], wv[NG * GP];
 #pragma unroll
-    for (int i = 0; i < NPK; ++i) {
-      Vals<W, V, 1> pw;
-      if (w) pw.load(w, c0 + i * cstep, 0, d);
+    for (int i = 0; i < NG; ++i) {
+      Vals<W, V, PG> pw;
+      if (w) pw.load(w, c0 + i * PG * cstep, cstep, d);
 #pragma unroll
-      for (int j = 0; j < HV; ++j) {
-        aw[i * HV + j] = ab[i * HV + j] = f2(0.f, 0.f);
-        wv[i * HV + j] = w ? pw.pair(j) : f2(1.f, 1.f);
+      for (int j = 0; j < GP; ++j) {
+        aw[i * GP + j] = ab[i * GP + j] = f2(0.f, 0.f);
+        wv[i * GP + j] = w ? pw.pair(j) : f2(1.f, 1.f);
       }
     }
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
-      const int rows = rows_of(t);
-      const uint8_t* base = smem + (size_t)st * stage_bytes;
+      const int rows = sg < nsg ? rows_of(t) : 0;   // threads past the last whole ct rest
       bounded_wait(&ready[st], phase, &s_abort, status, 8, WAIT_LIMIT_NS);
 #pragma unroll 2
       for (int r = sg; r < rows; r += nsg) {
+        const int64_t row = t * R + r;
         const F2 nmu = stat[st][r][0], rs2 = stat[st][r][1], ns1 = stat[st][r][2], ns2 = stat[st][r][3];
-        const T* xr = reinterpret_cast<const T*>(base + (size_t)r * rb);
-        const T* dr = reinterpret_cast<const T*>(base + (size_t)(R + r) * rb);
-        const T* ar = reinterpret_cast<const T*>(base + (size_t)(2 * R + r) * rb);
-        T* orow = dx + (t * R + r) * d;
+        const T *xr = in_stage(0, r, x + row * ldx), *dr = in_stage(1, r, dy + row * lddy);
+        const T* ar = in_stage(2, r, add + (add ? row * ldadd : 0));
+        T* orow = dx + row * d;
 #pragma unroll
-        for (int i = 0; i < NPK; ++i) {
-          const int c = c0 + i * cstep;
+        for (int i = 0; i < NG; ++i) {
+          const int c = c0 + i * PG * cstep;
           if (c < d) {
             P px, pd, pa, o;
-            px.load(xr, c, 0, d);
-            pd.load(dr, c, 0, d);
-            if (add) pa.load(ar, c, 0, d);
+            px.load(xr, c, cstep, d);
+            pd.load(dr, c, cstep, d);
+            if (add) pa.load(ar, c, cstep, d);
 #pragma unroll
-            for (int j = 0; j < HV; ++j) {
-              const int m = i * HV + j;
+            for (int j = 0; j < GP; ++j) {
+              const int m = i * GP + j;
               const F2 dyv = pd.pair(j);
               const F2 xh = f2_mul(f2_add(px.pair(j), nmu), rs2);
               aw[m] = f2_fma(dyv, xh, aw[m]);
@@ -523,7 +667,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
               const F2 e = f2_fma(xh, ns2, f2_fma(dyv, wv[m], ns1));
               o.set_pair(j, add ? f2_fma(e, rs2, pa.pair(j)) : f2_mul(e, rs2));
             }
-            o.store(orow, c, 0, d);
+            o.store(orow, c, cstep, d);
           }
         }
       }
@@ -533,7 +677,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
     if (part != nullptr) {
       // the row subgroups' sums, added in order; every stage has been read by
       // then, so its memory holds them
-      auto columns = []() { asm volatile("bar.sync 1, %0;" ::"n"(32 * LN_CW) : "memory"); };
+      auto columns = []() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CW) : "memory"); };
       float* acc = reinterpret_cast<float*>(smem);   // [2][d]
       float* pr = part + (size_t)blockIdx.x * 2 * d;
       columns();
@@ -541,20 +685,20 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
         if (sg == k) {
           float* to = k == nsg - 1 ? pr : acc;
 #pragma unroll
-          for (int m = 0; m < NPK * HV; ++m) {
-            const int c = c0 + m / HV * cstep + 2 * (m % HV);
-            if (c < d) {
-              float2 sw = f2_get(aw[m]), sb = f2_get(ab[m]);
-              if (k > 0) {
-                sw.x += acc[c];
-                sw.y += acc[c + 1];
-                sb.x += acc[d + c];
-                sb.y += acc[d + c + 1];
+          for (int m = 0; m < NG * GP; ++m) {
+            const float2 sw = f2_get(aw[m]), sb = f2_get(ab[m]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = Vals<T, V, NG * PG>::column(m, h, c0, cstep);
+              if (c < d) {
+                float u = h ? sw.y : sw.x, v = h ? sb.y : sb.x;
+                if (k > 0) {
+                  u += acc[c];
+                  v += acc[d + c];
+                }
+                to[c] = u;
+                to[d + c] = v;
               }
-              to[c] = sw.x;
-              to[c + 1] = sw.y;
-              to[d + c] = sb.x;
-              to[d + c + 1] = sb.y;
             }
           }
         }
@@ -698,6 +842,37 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
   return MOE_OK;
 }
 
+// k_ln_fwd_units' launch; 1 where it does not fit or there are too few rows.
+template <class T, class W>
+int ln_fwd_units(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, float eps, T* y,
+                 float* mean, float* rstd, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T), MAXNV = 32 / V;   // up to 32 columns per thread
+  if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15u) ||
+      (ldx - d) % V)
+    return 1;
+  const int units = (d + 2 * V - 2) / V;         // at most, over the offsets
+  int gw = 1;
+  while (gw < 8 && units > gw * 32 * MAXNV) gw *= 2;
+  if (units > gw * 32 * MAXNV || (int64_t)T_ * gw < LN_SMS * 64) return 1;
+  const size_t bytes = (size_t)2 * (d + d / 32 + 2) * sizeof(float);
+  const int per_sm = (int)std::min<size_t>(200 * 1024 / bytes, 4);
+  const int64_t want = ((int64_t)T_ * gw + 7) / 8;
+  const int grid = (int)std::min<int64_t>(want, LN_SMS * per_sm);
+  ProfScope _ps("layernorm_fwd", s);
+#define LN_GO(NV)                                                                              \
+  do {                                                                                         \
+    if (cudaError_t e = smem_limit<k_ln_fwd_units<T, W, NV>>(72 * 1024))                       \
+      return cuda_fail(e, "layernorm smem attribute");                                         \
+    k_ln_fwd_units<T, W, NV><<<grid, 256, bytes, s>>>(x, ldx, w, b, y, mean, rstd, T_, d,      \
+                                                      1.0f / (float)d, eps, gw);               \
+  } while (0)
+  if (units <= gw * 32 * MAXNV / 2) LN_GO(MAXNV / 2);
+  else LN_GO(MAXNV);
+#undef LN_GO
+  MOE_CHECK_LAUNCH("layernorm_fwd");
+  return MOE_OK;
+}
+
 template <class T, class W>
 int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, int d, float eps,
              void* y, float* mean, float* rstd, cudaStream_t s) {
@@ -705,6 +880,10 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
   const W *wt = (const W*)w, *bt = (const W*)b;
   T* yt = (T*)y;
   const int v = pick_pack<T, W>(d, {ldx}, {x, y}, {w, b});
+  if (v * (int)sizeof(T) < 16) {
+    const int rc = ln_fwd_units<T, W>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
+    if (rc <= 0) return rc;
+  }
   if constexpr (sizeof(T) == 2) {
     if (v == 8) return ln_fwd_v<T, W, 8>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
     if (v == 2) return ln_fwd_v<T, W, 2>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
@@ -717,51 +896,63 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
 constexpr int LN_COLS = 8192;     // widest row of k_ln_bwd: 8 columns x 1024 threads
 constexpr int LN_PARTS = 148 * 4;    // most blocks of either kernel
 constexpr int LN_SLICES = 64;     // row slices of k_ln_bwd_cols
-// Launch shape of k_ln_bwd_ws; R = 0 where rows are not of 16-byte units or too
-// few to give every block a few stages.
+// Launch shape of k_ln_bwd_ws for packs of v; R = 0 where rows are too wide or
+// too few to give every block a few stages.
 struct LnWs {
-  int R = 0, stages, ct, npk, grid;
+  int R = 0, stages, ct, E, cw, grid;
   size_t bytes;
 };
-LnWs ln_bwd_ws(int T_, int d, int es, bool add) {
+LnWs ln_bwd_ws(int T_, int d, int es, int v, bool add) {
   LnWs p;
-  const int v = 16 / es;
-  if (d % v || d > LN_COLS) return p;
-  const int packs = d / v;
-  p.ct = 32;
-  while (p.ct < 32 * LN_CW && p.ct < packs) p.ct *= 2;
-  p.npk = (packs + p.ct - 1) / p.ct;
-  // two blocks per SM where the columns' registers allow it; stages of at
-  // least four rows (a row per warp) where three of them fit
-  const size_t rb = (size_t)d * es * (add ? 3 : 2), room = (p.npk == 1 ? 108 : 216) * 1024;
-  int r = 8;
-  while (r > 4 && 3 * r * rb > room) r /= 2;
-  while (r > 1 && 2 * r * rb > room) r /= 2;
-  p.stages = (int)std::min<size_t>(room / (r * rb), LN_STAGES);
-  p.grid = LN_SMS * (p.npk == 1 ? 2 : 1);
-  p.bytes = std::max((size_t)p.stages * r * rb, (size_t)8 * d);
+  if (d > LN_COLS) return p;
+  // 8 column warps and two blocks per SM for up to 8 columns per thread, 16
+  // warps and one block beyond; as few columns per thread as there are threads
+  p.cw = (d + 255) / 256 <= 8 ? 8 : 16;
+  p.E = std::max(v == 1 ? 2 : v, es == 4 && v > 1 ? 4 : 2);
+  while ((d + p.E - 1) / p.E > 32 * p.cw) p.E *= 2;
+  p.ct = ((d + p.E - 1) / p.E + 31) / 32 * 32;
+  // stages of at least a row per row-sum warp where three of them fit
+  const int sw = ln_sum_warps(p.cw);
+  const size_t rb = v == 1 ? ((size_t)d * es + 15) / 16 * 16 + 16 : (size_t)d * es;
+  const size_t row = rb * (add ? 3 : 2), room = (p.cw == 8 ? 108 : 216) * 1024;
+  int r = 2 * sw;
+  if (3 * r * row > room) r = sw;
+  while (r > 1 && 2 * r * row > room) --r;
+  p.stages = (int)std::min<size_t>(room / (r * row), LN_STAGES);
+  p.grid = LN_SMS * (p.cw == 8 ? 2 : 1);
+  p.bytes = std::max((size_t)p.stages * r * row, (size_t)8 * d);
   if (p.stages < 2 || T_ < 4 * (int64_t)p.grid * r) return p;
   p.R = r;
   return p;
 }
 
-template <class T, class W>
+template <class T, class W, int V>
 int ln_bwd_ws_go(const LnWs& p, const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w,
                  const float* mean, const float* rstd, const T* add, int64_t ldadd, int T_, int d,
                  T* dx, float* part, cudaStream_t s) {
   ProfScope _ps("layernorm_bwd", s);
-#define LN_GO(NPK)                                                                             \
+#define LN_GO(E, CW)                                                                           \
   do {                                                                                         \
-    if (cudaError_t e = smem_limit<k_ln_bwd_ws<T, W, NPK>>(216 * 1024))                        \
+    if (cudaError_t e = smem_limit<k_ln_bwd_ws<T, W, V, E, CW>>((CW == 8 ? 108 : 216) * 1024)) \
       return cuda_fail(e, "layernorm smem attribute");                                         \
-    k_ln_bwd_ws<T, W, NPK><<<p.grid, LN_WS_THREADS, p.bytes, s>>>(                             \
+    k_ln_bwd_ws<T, W, V, E, CW><<<p.grid, ln_ws_threads(CW), p.bytes, s>>>(                  \
         dy, lddy, x, ldx, w, mean, rstd, add, ldadd, dx, part, T_, d, 1.0f / (float)d, p.R,    \
         p.stages, p.ct, status_ptr());                                                         \
   } while (0)
-  if (p.npk <= 1) LN_GO(1);
-  else if (p.npk <= 2) LN_GO(2);
-  else if (sizeof(T) == 2 || p.npk <= 4) LN_GO(4);
-  else if constexpr (sizeof(T) == 4) LN_GO(8);
+  if (p.cw == 16) {
+    if (p.E <= 8) LN_GO(8, 16);
+    else LN_GO(16, 16);
+  } else if constexpr (V == 8) {
+    LN_GO(8, 8);
+  } else {
+    if (p.E <= 2) {
+      if constexpr (V == 1) LN_GO(2, 8);
+    } else if (p.E <= 4) {
+      LN_GO(4, 8);
+    } else {
+      LN_GO(8, 8);
+    }
+  }
 #undef LN_GO
   MOE_CHECK_LAUNCH("layernorm_bwd");
   return MOE_OK;
@@ -771,11 +962,11 @@ template <class T, class W, int V>
 int ln_bwd_v(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, const float* mean,
              const float* rstd, const T* add, int64_t ldadd, int T_, int d, T* dx, float* part,
              int* nparts, cudaStream_t s) {
-  if constexpr (V * sizeof(T) == 16) {
-    const LnWs p = ln_bwd_ws(T_, d, sizeof(T), add != nullptr);
+  if constexpr (V * sizeof(T) == 16 || V == 1) {
+    const LnWs p = ln_bwd_ws(T_, d, sizeof(T), V, add != nullptr);
     if (p.R) {
       *nparts = p.grid;
-      return ln_bwd_ws_go<T, W>(p, dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T_, d, dx, part, s);
+      return ln_bwd_ws_go<T, W, V>(p, dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T_, d, dx, part, s);
     }
   }
   const int G = ((d + 7) / 8 + 31) / 32 * 32, groups = G >= 128 ? 1 : 128 / G, block = G * groups;
@@ -821,7 +1012,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
   return ln_bwd_v<T, W, V>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, T_, d, dxt, part, nparts, s)
   if constexpr (sizeof(T) == 2) {
     if (v == 8) LN_V(8);
-    if (v == 2) LN_V(2);
+    if (v == 2 && ln_bwd_ws(T_, d, 2, 1, add != nullptr).R == 0) LN_V(2);
   } else {
     if (v == 4) LN_V(4);
   }

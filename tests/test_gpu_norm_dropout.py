@@ -80,7 +80,8 @@ def check_ln(x, w, b, eps=1e-5, dy=None, add=None):
 SHAPES = [(1, 1), (1, 7168), (3, 2), (5, 31), (64, 33), (129, 128), (300, 250), (17, 1000), (37, 1037),
           (1000, 256), (450, 2048), (700, 1536), (40, 4096), (33, 4104), (20, 7168), (9, 8191),
           (12, 8192), (3, 8200), (2, 12345), (2, 70000), (4000, 64), (3001, 256), (2999, 1536), (1500, 2048),
-          (2500, 2056), (800, 4096), (700, 7168), (650, 8192), (620, 8184), (5000, 2048), (4800, 512), (9500, 128), (2600, 7168), (1300, 8192)]
+          (2500, 2056), (800, 4096), (700, 7168), (650, 8192), (620, 8184), (5000, 2048), (4800, 512), (9500, 128), (2600, 7168), (1300, 8192),
+          (9600, 33), (5000, 339), (3000, 1037), (3100, 1038), (2400, 2046), (1300, 4341), (2500, 7017), (1250, 8183)]
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
@@ -110,6 +111,30 @@ def test_layernorm_row_strides_and_alignment(dtype, d, pad, skip):
     check_ln(cut(), draw(gen, d), draw(gen, d), dy=cut(), add=cut())
     # weights that start at an odd element
     check_ln(cut(), draw(gen, d + 1)[1:], draw(gen, d + 1)[1:], dy=cut(), add=cut())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d,pad,skip", [(9600, 128, 3, 1), (3000, 1000, 8, 4), (3000, 1001, 8, 3), (3000, 1001, 5, 0)])
+def test_layernorm_many_rows_inside_a_wider_matrix(T, d, pad, skip, dtype):
+    """Each array at an offset of its own, NaN all around the rows."""
+    gen = torch.Generator().manual_seed(T + d + pad + skip)
+
+    def cut(k):
+        big = torch.full((T + 2, d + pad + 8), float("nan"), dtype=dtype, device="cuda")
+        view = big[1:T + 1, k:k + d]
+        view.copy_(draw(gen, T, d, dtype=dtype))
+        return view
+
+    check_ln(cut(skip), draw(gen, d), draw(gen, d), dy=cut((skip + 1) % 8), add=cut((2 * skip + 5) % 8))
+    # x and y at the same offset in their 16 bytes
+    x = cut(skip)
+    if (x.stride(0) - d) % 8 == 0:
+        buf = torch.full((T * d + 32,), 7.0, dtype=dtype, device="cuda")
+        off = (x.data_ptr() - buf.data_ptr()) // x.element_size() % (16 // x.element_size())
+        y = B.moe_layernorm_fwd(x, y=buf[off:off + T * d].view(T, d))[0]
+        ref = O.layernorm_fwd(f64(x), None, None, 1e-5)[0]
+        within(y, ref, 256 * U * (np.abs(ref) + 2) + half_step(dtype) * np.abs(ref), "y")
+        assert (buf[:off] == 7).all() and (buf[off + T * d:] == 7).all()
 
 
 def test_layernorm_offset_does_not_cancel():
