@@ -229,14 +229,13 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
 // walked in the 16-byte units that hold it: unit j holds columns V j - o ..,
 // o the row's offset in its first unit; columns outside the row count as
 // nothing, and whole units leave as one store.  The columns of a thread thus
-// move from row to row, so w and b lie in shared memory as fp32, skewed by one
-// word in 32 (column c at c + c / 32), which spreads a warp's reads of every
-// V-th column over the banks.  Persistent blocks of 8 warps, gw to a row.
-// 32000 x 1037 bf16 in XX us; by single elements 129.
-__device__ __forceinline__ int ln_skew(int c) { return c + (c >> 5); }
-
+// move from row to row, so w and b lie in shared memory as fp32, V columns and
+// a word to spare: element k of unit j is word (V + 1) j - o + k, less one
+// where k < o (a choice that the whole row shares), and a warp's 32 units hit
+// 32 banks.  Persistent blocks of 8 warps, gw to a row.  32000 x 1037 bf16 in
+// 60 us; by single elements 129.
 template <class T, class W, int NV>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
                float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float inv_d,
                float eps, int gw) {
@@ -246,10 +245,11 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
   typedef Vals<T, V, 1> P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp / gw, groups = 8 / gw, lin = (warp % gw) * 32 + lane, G = gw * 32;
-  float *sw = params, *sb = params + ln_skew(d) + 1;
+  float *sw = params, *sb = params + (d / V + 1) * (V + 1);
   for (int c = threadIdx.x; c < d; c += 256) {
-    if (w) sw[ln_skew(c)] = to_f(w[c]);
-    if (b) sb[ln_skew(c)] = to_f(b[c]);
+    const int i = c / V * (V + 1) + c % V;
+    if (w) sw[i] = to_f(w[c]);
+    if (b) sb[i] = to_f(b[c]);
   }
   __syncthreads();
   auto sum = [&](float v, float* r) {            // over the row's warps
@@ -311,15 +311,17 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
     const F2 rs2 = f2(rs, rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lin + i * G) * V - o;
+      const int base = (lin + i * G) * (V + 1) - o;   // word of element k: base + k - (k < o)
+      auto word = [&](const float* p, int k) { return (k < o ? p + base - 1 : p + base)[k]; };
       if (in(i, 0) && in(i, V - 1)) {
         P out;
 #pragma unroll
         for (int j = 0; j < HV; ++j) {
-          const int s0 = ln_skew(c + 2 * j), s1 = ln_skew(c + 2 * j + 1);
           F2 e = f2_mul(v[i * HV + j], rs2);
-          if (w) e = f2_mul(e, f2(sw[s0], sw[s1]));
-          if (b) e = f2_add(e, f2(sb[s0], sb[s1]));
+          if (w && b) e = f2_fma(e, f2(word(sw, 2 * j), word(sw, 2 * j + 1)),
+                                 f2(word(sb, 2 * j), word(sb, 2 * j + 1)));
+          else if (w) e = f2_mul(e, f2(word(sw, 2 * j), word(sw, 2 * j + 1)));
+          else if (b) e = f2_add(e, f2(word(sb, 2 * j), word(sb, 2 * j + 1)));
           out.set_pair(j, e);
         }
         out.store(ya, (lin + i * G) * V, 0, o + d);
@@ -330,8 +332,9 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
           if (in(i, k)) {
             const float2 t = f2_get(v[i * HV + k / 2]);
             float e = (k & 1 ? t.y : t.x) * rs;
-            if (w) e *= sw[ln_skew(c + k)];
-            if (b) e += sb[ln_skew(c + k)];
+            if (w && b) e = fmaf(e, word(sw, k), word(sb, k));
+            else if (w) e *= word(sw, k);
+            else if (b) e += word(sb, k);
             ya[(lin + i * G) * V + k] = from_f<T>(e);
           }
       }
@@ -505,12 +508,13 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
 // threads neighbouring columns.
 constexpr int LN_STAGES = 6;                     // at most
 // Row-sum warps: with 16 column warps three, so that 20 warps leave each
-// thread 96 registers.
-constexpr int ln_sum_warps(int cw) { return cw == 16 ? 3 : 4; }
-constexpr int ln_ws_threads(int cw) { return 32 * (cw + ln_sum_warps(cw) + 1); }
+// thread 96 registers; single bf16 elements need more of them (9563 x 7017:
+// 212 us with 7, 280 with 3; fp32 loses by it, 6000 x 4341: 140 and 113).
+constexpr int ln_sum_warps(int cw, int v, int es) { return cw == 16 ? (v == 1 && es == 2 ? 7 : 3) : 4; }
+constexpr int ln_ws_threads(int cw, int v, int es) { return 32 * (cw + ln_sum_warps(cw, v, es) + 1); }
 
 template <class T, class W, int V, int E, int CW>
-__global__ void __launch_bounds__(ln_ws_threads(CW), CW == 8 ? 2 : 1)
+__global__ void __launch_bounds__(ln_ws_threads(CW, V, sizeof(T)), CW == 8 ? 2 : 1)
 k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
             const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
             int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, float inv_d, int R,
@@ -520,7 +524,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
   // per row of a stage, as pairs of the same value: -mean, rstd, -s1 / d, -s2 / d
   __shared__ __align__(16) F2 stat[LN_STAGES][8][4];
   __shared__ volatile int s_abort;
-  constexpr int SW = ln_sum_warps(CW);
+  constexpr int SW = ln_sum_warps(CW, V, sizeof(T));
   constexpr int PG = V == 1 ? 2 : 1;             // packs at a time: a pair at least
   typedef Vals<T, V, PG> P;
   constexpr int NG = E / (V * PG), GP = P::NP;   // groups of packs per thread, pairs in one
@@ -582,15 +586,16 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
     }
   } else if (warp >= CW) {
     // ------------------------------------------------------------ the rows' sums
+    // the block's rows go round the warps, across the stages
+    int turn = warp - CW;                          // this warp's first row of the stage
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
       const int rows = rows_of(t);
-      const int64_t r0 = t * R + warp - CW;   // this warp's first row: its statistics early
-      const bool any = warp - CW < rows;
-      const float mu0 = any ? mean[r0] : 0.f, rs0 = any ? rstd[r0] : 0.f;
+      const bool any = turn < rows;                // its statistics early
+      const float mu0 = any ? mean[t * R + turn] : 0.f, rs0 = any ? rstd[t * R + turn] : 0.f;
       // a warp without a row waits too: it must not run ahead of the stage
       bounded_wait(&full[st], phase, &s_abort, status, 7, WAIT_LIMIT_NS);
-      for (int r = warp - CW; r < rows; r += SW) {
-        const bool first = r == warp - CW;
+      for (int r = turn; r < rows; r += SW) {
+        const bool first = r == turn;
         const int64_t row = t * R + r;
         const float mu = first ? mu0 : mean[row], rs = first ? rs0 : rstd[row];
         const F2 nmu = f2(-mu, -mu);
@@ -622,6 +627,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[st]);
+      turn = (turn + SW - R % SW) % SW;            // all stages but the last hold R rows
     }
   } else {
     // ------------------------------------------------------------ dx and the columns' sums
@@ -807,12 +813,12 @@ template <class T, class W, int V>
 int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, float eps, T* y,
              float* mean, float* rstd, cudaStream_t s) {
   const int npack = d / V;
-  // Warps per row: as few as hold the row in 4 packs a thread (16384 x 2048
-  // bf16: 2 warps 36 us, 1 warp with 8 packs 44, 4 warps 38); more while the
-  // rows alone do not give the SMs 16 warps each (few rows: latency).  Rows
-  // past 32 warps of 4 take 8 packs.
+  // Warps per row: as few as hold the row in 32 columns a thread (16384 x 2048
+  // bf16: 2 warps 36 us, 1 warp with 64 columns 44, 4 warps 38); more while
+  // the rows alone do not give the SMs 16 warps each (few rows: latency).
+  constexpr int PT = V * sizeof(T) == 16 ? 32 / V : 4;
   int wpr = 1;
-  while (wpr < 32 && npack > wpr * 32 * 4) wpr *= 2;
+  while (wpr < 32 && npack > wpr * 32 * PT) wpr *= 2;
   while (wpr < 32 && npack > wpr * 32 && (int64_t)T_ * wpr < LN_SMS * 16) wpr *= 2;
   const int nv = (npack + wpr * 32 - 1) / (wpr * 32);
   const float inv_d = 1.0f / (float)d;
@@ -833,7 +839,10 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
     else LN_GO(NV, 32);                                                                       \
   } while (0)
   if (nv > 8) k_ln_fwd_wide<T, W><<<T_, 1024, 0, s>>>(x, ldx, w, b, y, mean, rstd, d, eps);
-  else if (nv > 4) LN_GO(8, 32);
+  else if (nv > 4) {
+    if constexpr (PT == 8) LN_W(8);
+    else LN_GO(8, 32);
+  }
   else if (nv > 2) LN_W(4);
   else LN_W(2);
 #undef LN_W
@@ -846,27 +855,30 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
 template <class T, class W>
 int ln_fwd_units(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, float eps, T* y,
                  float* mean, float* rstd, cudaStream_t s) {
-  constexpr int V = 16 / (int)sizeof(T), MAXNV = 32 / V;   // up to 32 columns per thread
+  constexpr int V = 16 / (int)sizeof(T), MAXNV = 40 / V;   // up to 40 columns per thread
   if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15u) ||
       (ldx - d) % V)
     return 1;
   const int units = (d + 2 * V - 2) / V;         // at most, over the offsets
   int gw = 1;
   while (gw < 8 && units > gw * 32 * MAXNV) gw *= 2;
-  if (units > gw * 32 * MAXNV || (int64_t)T_ * gw < LN_SMS * 64) return 1;
-  const size_t bytes = (size_t)2 * (d + d / 32 + 2) * sizeof(float);
-  const int per_sm = (int)std::min<size_t>(200 * 1024 / bytes, 4);
+  if (units > gw * 32 * MAXNV || (int64_t)T_ * gw < LN_SMS * 8) return 1;
+  const size_t bytes = (size_t)2 * (d / V + 1) * (V + 1) * sizeof(float);
+  const int per_sm = (int)std::min<size_t>(216 * 1024 / bytes, 3);
   const int64_t want = ((int64_t)T_ * gw + 7) / 8;
   const int grid = (int)std::min<int64_t>(want, LN_SMS * per_sm);
   ProfScope _ps("layernorm_fwd", s);
 #define LN_GO(NV)                                                                              \
   do {                                                                                         \
-    if (cudaError_t e = smem_limit<k_ln_fwd_units<T, W, NV>>(72 * 1024))                       \
+    if (cudaError_t e = smem_limit<k_ln_fwd_units<T, W, NV>>(100 * 1024))                      \
       return cuda_fail(e, "layernorm smem attribute");                                         \
     k_ln_fwd_units<T, W, NV><<<grid, 256, bytes, s>>>(x, ldx, w, b, y, mean, rstd, T_, d,      \
                                                       1.0f / (float)d, eps, gw);               \
   } while (0)
-  if (units <= gw * 32 * MAXNV / 2) LN_GO(MAXNV / 2);
+  const int nv = (units + gw * 32 - 1) / (gw * 32);
+  if (nv * 5 <= MAXNV * 2) LN_GO(MAXNV * 2 / 5);
+  else if (nv * 5 <= MAXNV * 3) LN_GO(MAXNV * 3 / 5);
+  else if (nv * 5 <= MAXNV * 4) LN_GO(MAXNV * 4 / 5);
   else LN_GO(MAXNV);
 #undef LN_GO
   MOE_CHECK_LAUNCH("layernorm_fwd");
@@ -911,17 +923,17 @@ LnWs ln_bwd_ws(int T_, int d, int es, int v, bool add) {
   p.E = std::max(v == 1 ? 2 : v, es == 4 && v > 1 ? 4 : 2);
   while ((d + p.E - 1) / p.E > 32 * p.cw) p.E *= 2;
   p.ct = ((d + p.E - 1) / p.E + 31) / 32 * 32;
-  // stages of at least a row per row-sum warp where three of them fit
-  const int sw = ln_sum_warps(p.cw);
+  // stages of a row or two per row-sum warp where three of them fit
+  const int sw = ln_sum_warps(p.cw, v, es);
   const size_t rb = v == 1 ? ((size_t)d * es + 15) / 16 * 16 + 16 : (size_t)d * es;
   const size_t row = rb * (add ? 3 : 2), room = (p.cw == 8 ? 108 : 216) * 1024;
-  int r = 2 * sw;
-  if (3 * r * row > room) r = sw;
+  p.grid = LN_SMS * (p.cw == 8 ? 2 : 1);
+  int r = std::min(2 * sw, 8);
+  if (3 * r * row > room || T_ < 4 * (int64_t)p.grid * r) r = std::min(sw, 4);
   while (r > 1 && 2 * r * row > room) --r;
   p.stages = (int)std::min<size_t>(room / (r * row), LN_STAGES);
-  p.grid = LN_SMS * (p.cw == 8 ? 2 : 1);
   p.bytes = std::max((size_t)p.stages * r * row, (size_t)8 * d);
-  if (p.stages < 2 || T_ < 4 * (int64_t)p.grid * r) return p;
+  if (p.stages < 2 || T_ < 2 * (int64_t)p.grid * r) return p;
   p.R = r;
   return p;
 }
@@ -935,7 +947,7 @@ int ln_bwd_ws_go(const LnWs& p, const T* dy, int64_t lddy, const T* x, int64_t l
   do {                                                                                         \
     if (cudaError_t e = smem_limit<k_ln_bwd_ws<T, W, V, E, CW>>((CW == 8 ? 108 : 216) * 1024)) \
       return cuda_fail(e, "layernorm smem attribute");                                         \
-    k_ln_bwd_ws<T, W, V, E, CW><<<p.grid, ln_ws_threads(CW), p.bytes, s>>>(                  \
+    k_ln_bwd_ws<T, W, V, E, CW><<<p.grid, ln_ws_threads(CW, V, sizeof(T)), p.bytes, s>>>(                  \
         dy, lddy, x, ldx, w, mean, rstd, add, ldadd, dx, part, T_, d, 1.0f / (float)d, p.R,    \
         p.stages, p.ct, status_ptr());                                                         \
   } while (0)
