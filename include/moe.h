@@ -516,8 +516,8 @@ int moe_dropout_bwd(const void* dout, int64_t n, double p, const int64_t* rng, i
  *   output, joined in the last product's epilogue) or NULL; H [T,2f] out, for
  *   the backward pass, or NULL (serving: not written); y [T,d] out; y may be
  *   addend itself.  bf16 only, fp32 accumulation, H and A each rounded
- *   once to bf16 (A from the unrounded H).  T >= 0; d and f multiples of 8 (<= 2^20); all pointers 16-byte
- *   aligned.  ws: at least moe_shared_ffn_fwd_workspace_size() bytes.  Needs
+ *   once to bf16 (A from the unrounded H).  T >= 0; d and f multiples of 8, no matrix over 2^38 elements;
+ *   all pointers 16-byte aligned.  ws: at least moe_shared_ffn_fwd_workspace_size() bytes.  Needs
  *   an sm_100 device.
  * moe_shared_ffn_bwd -- from dout and the saved x and H, with A recomputed:
  *   dA = dout W2^T, dH = [dA*H3*silu'(H1) | dA*silu(H1)],

@@ -951,14 +951,15 @@ static int check_ffn(int T, int d, int f, int dtype) {
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0");
   if (d <= 0 || d % 8) return fail(MOE_ERR_UNSUPPORTED, "d must be a positive multiple of 8");
   if (f <= 0 || f % 8) return fail(MOE_ERR_UNSUPPORTED, "f must be a positive multiple of 8");
-  if (d > (1 << 20) || f > (1 << 20) || T > (1 << 30))
-    return fail(MOE_ERR_UNSUPPORTED, "d and f must be <= 2^20, T <= 2^30");
+  const int64_t most = (int64_t)1 << 38;   // elements of a matrix: tile counts stay within 32 bits
+  if (T > (1 << 30) || (int64_t)T * d > most || (int64_t)T * f > most || (int64_t)d * f > most)
+    return fail(MOE_ERR_UNSUPPORTED, "T must be <= 2^30 and every matrix <= 2^38 elements");
   if (!tc_available()) return fail(MOE_ERR_UNSUPPORTED, "the shared FFN needs an sm_100 device");
   return MOE_OK;
 }
 
 size_t moe_shared_ffn_fwd_workspace_size(int T, int d, int f, int dtype) {
-  if (T <= 0 || d <= 0 || f <= 0 || dtype != MOE_BF16) return 0;
+  if (T <= 0 || check_ffn(T, d, f, dtype)) return 0;
   Sizer z;
   SharedFwdWs<Sizer> w;
   w.carve(z, T, d, f);
@@ -985,7 +986,7 @@ int moe_shared_ffn_fwd(const void* x, const void* w1, const void* w3, const void
 }
 
 size_t moe_shared_ffn_bwd_workspace_size(int T, int d, int f, int dtype) {
-  if (T <= 0 || d <= 0 || f <= 0 || dtype != MOE_BF16) return 0;
+  if (T <= 0 || check_ffn(T, d, f, dtype)) return 0;
   Sizer z;
   SharedBwdWs<Sizer> w;
   w.carve(z, T, d, f);

@@ -906,7 +906,7 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
 }
 
 constexpr int LN_COLS = 8192;     // widest row of k_ln_bwd: 8 columns x 1024 threads
-constexpr int LN_PARTS = 148 * 4;    // most blocks of either kernel
+constexpr int LN_PARTS = LN_SMS * 4;   // most blocks of either kernel
 constexpr int LN_SLICES = 64;     // row slices of k_ln_bwd_cols
 // Launch shape of k_ln_bwd_ws for packs of v; R = 0 where rows are too wide or
 // too few to give every block a few stages.
@@ -984,7 +984,8 @@ int ln_bwd_v(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, con
   const int G = ((d + 7) / 8 + 31) / 32 * 32, groups = G >= 128 ? 1 : 128 / G, block = G * groups;
   const size_t smem = groups > 1 ? (size_t)2 * d * sizeof(float) : 0;
   const int64_t steps = ((int64_t)T_ + groups - 1) / groups;
-  const int grid = (int)std::min<int64_t>(steps, LN_SMS * (block <= 512 ? 512 / block : 1));
+  const int per_sm = std::min(4, block <= 512 ? 512 / block : 1);   // LN_PARTS allows for 4
+  const int grid = (int)std::min<int64_t>(steps, LN_SMS * per_sm);
   *nparts = grid;
   ProfScope _ps("layernorm_bwd", s);
 #define LN_GO(MAXT)                                                         \

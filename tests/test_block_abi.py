@@ -88,7 +88,7 @@ def ffn_bwd(**kw):
 
 
 SHARED = [(dict(dt=B.MOE_F32), -2), (dict(T=-1), -1), (dict(d=12), -2), (dict(f=4), -2), (dict(d=0), -2),
-          (dict(f=-8), -2), (dict(d=1 << 21), -2), (dict(x=None), -1), (dict(w1=None), -1), (dict(w3=None), -1),
+          (dict(f=-8), -2), (dict(T=1 << 30, d=1 << 20), -2), (dict(d=1 << 20, f=1 << 20), -2), (dict(x=None), -1), (dict(w1=None), -1), (dict(w3=None), -1),
           (dict(w2=None), -1), (dict(x=ctypes.c_void_p(264)), -1), (dict(w2=ctypes.c_void_p(258)), -1),
           (dict(add=ctypes.c_void_p(258)), -1), (dict(ws=None), -1), (dict(wsb=8), -5)]
 
@@ -107,6 +107,7 @@ def test_shared_ffn_bwd_refusals(kw, code):
 def test_shared_ffn_workspaces():
     for size in (B.lib().moe_shared_ffn_fwd_workspace_size, B.lib().moe_shared_ffn_bwd_workspace_size):
         assert size(0, 256, 128, B.MOE_BF16) == 0 and size(10, 256, 128, B.MOE_F32) == 0
+        assert size(1 << 30, 1 << 20, 128, B.MOE_BF16) == 0 and size(10, 12, 128, B.MOE_BF16) == 0
         assert 0 < size(10, 256, 128, B.MOE_BF16) < size(10000, 256, 128, B.MOE_BF16)
 
 
@@ -121,3 +122,12 @@ def test_binding_refuses_ffn_arguments():
                  lambda: B.moe_shared_ffn_bwd(x, x, w1, w1, w2, torch.zeros(4, 8, dtype=bf))):
         with pytest.raises(B.MoEError):
             call()
+
+
+def test_layernorm_workspace_covers_every_launch_shape():
+    # one partial row of 2 d floats per block, 592 blocks at most (8192 columns)
+    size = B.lib().moe_layernorm_bwd_workspace_size
+    assert size(0, 700) == 0
+    for d in (1, 33, 700, 1037, 4096, 8192):
+        assert size(5, d) == 5 * 2 * d * 4 and size(100000, d) == 592 * 2 * d * 4
+    assert size(1, 8193) == 64 * 2 * 8193 * 4

@@ -180,7 +180,8 @@ def test_layernorm_in_place_and_no_rows(dtype):
 def test_layernorm_same_result_every_time_and_guarded_outputs():
     """Deterministic column sums; nothing is written outside the outputs."""
     gen = torch.Generator().manual_seed(8)
-    for T, d, dtype in ((1000, 1037, F32), (3000, 256, BF16), (200, 2048, BF16)):
+    for T, d, dtype in ((1000, 1037, F32), (3000, 256, BF16), (200, 2048, BF16), (1000, 700, BF16), (2000, 601, F32),
+                        (900, 768, F32), (3000, 2047, BF16), (1300, 7015, BF16), (700, 8192, F32)):
         x, dy, w = draw(gen, T, d, dtype=dtype), draw(gen, T, d, dtype=dtype), draw(gen, d)
         _, mean, rstd = B.moe_layernorm_fwd(x, w)
         first = B.moe_layernorm_bwd(dy, x, w, mean, rstd)

@@ -100,8 +100,16 @@ def test_exact_many_rows(T, d, f):
     for n, got in dict(g, y=y).items():
         assert ((ref[n].to(BF).double() == ref[n]).double().mean()) > 0.99, n
         assert torch.equal(got, ref[n].to(BF)), n
-    again = B.moe_shared_ffn_bwd(c["dout"], c["x"], c["w1"], c["w3"], c["w2"], H, addend=c["add"])
+    # the results where the addends were, and without an addend
+    w = (c["w1"], c["w3"], c["w2"])
+    a = c["add"].clone()
+    assert torch.equal(B.moe_shared_ffn_fwd(c["x"], *w, addend=a, y=a, save=False)[0], y)
+    a = c["add"].clone()
+    again = B.moe_shared_ffn_bwd(c["dout"], c["x"], *w, H, addend=a, out=dict(dx=a))
     assert all(torch.equal(again[n], g[n]) for n in g)
+    y = B.moe_shared_ffn_fwd(c["x"], *w)[0]
+    dx = B.moe_shared_ffn_bwd(c["dout"], c["x"], *w, H)["dx"]
+    assert torch.equal(y, (A @ w2).to(BF)) and torch.equal(dx, (d1 @ w1.T + d3 @ w3.T).to(BF))
 
 
 def random_case(T, d, f, seed, scale=1.0):
@@ -248,8 +256,8 @@ def test_guard_bands_and_dirty_workspaces(T, d, f):
     assert (ws1[n1:] == 0xFF).all() and (ws2[n2:] == 0xFF).all()
 
 
-def test_captured_graph_replays_on_new_inputs_and_another_stream():
-    T, d, f = 260, 512, 256
+@pytest.mark.parametrize("T,d,f", [(1, 256, 128), (260, 512, 256), (3000, 1024, 2048)])
+def test_captured_graph_replays_on_new_inputs_and_another_stream(T, d, f):
     a, b = random_case(T, d, f, 6), random_case(T, d, f, 7)
     names = ("x", "w1", "w3", "w2")
     wsf = torch.empty(B.lib().moe_shared_ffn_fwd_workspace_size(T, d, f, B.MOE_BF16), device="cuda", dtype=torch.uint8)
