@@ -476,6 +476,8 @@ int moe_balance_loss(const int32_t* idx, const float* gate, int T, int E, int k,
  *   T = 0.  Sums run in a fixed order (deterministic).  ws: at least
  *   moe_layernorm_bwd_workspace_size() bytes, 16-byte aligned (not needed
  *   without dweight and dbias).
+ *   Both calls may read a row in the 16-byte units that hold it; the other
+ *   bytes of its first and last unit do not reach the results.
  */
 int moe_layernorm_fwd(const void* x, int64_t ldx, const void* weight, const void* bias, int T,
                       int d, int dtype, int wdtype, float eps, void* y, float* mean, float* rstd,
@@ -516,9 +518,10 @@ int moe_dropout_bwd(const void* dout, int64_t n, double p, const int64_t* rng, i
  *   output, joined in the last product's epilogue) or NULL; H [T,2f] out, for
  *   the backward pass, or NULL (serving: not written); y [T,d] out; y may be
  *   addend itself.  bf16 only, fp32 accumulation, H and A each rounded
- *   once to bf16 (A from the unrounded H).  T >= 0; d and f multiples of 8, no matrix over 2^38 elements;
- *   all pointers 16-byte aligned.  ws: at least moe_shared_ffn_fwd_workspace_size() bytes.  Needs
- *   an sm_100 device.
+ *   once to bf16 (A from the unrounded H).  0 <= T <= 2^30; d and f multiples
+ *   of 8, at most 2^28; no matrix over 2^38 elements; all pointers 16-byte
+ *   aligned.  ws: at least moe_shared_ffn_fwd_workspace_size() bytes (0 for
+ *   sizes that the call refuses).  Needs an sm_100 device.
  * moe_shared_ffn_bwd -- from dout and the saved x and H, with A recomputed:
  *   dA = dout W2^T, dH = [dA*H3*silu'(H1) | dA*silu(H1)],
  *   dx = dH [W1 | W3]^T + addend (addend [T,d], e.g. the routed experts' dx,

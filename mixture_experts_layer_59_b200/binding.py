@@ -535,6 +535,8 @@ def _matrix(name, t):
     """(rows, columns, dtype code) of a matrix of a supported dtype."""
     if t.dim() != 2:
         _bad(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    if max(t.shape) > 0x7fffffff:
+        _bad(f"{name}: {tuple(t.shape)} has more than 2^31 - 1 rows or columns", MOE_ERR_UNSUPPORTED)
     return (*t.shape, _code(name, t))
 
 

@@ -875,6 +875,8 @@ int moe_layernorm_fwd(const void* x, int64_t ldx, const void* weight, const void
   REQUIRE_ELEM_ALIGNED(y, esize(dtype));
   REQUIRE_ELEM_ALIGNED(weight, esize(wdtype));
   REQUIRE_ELEM_ALIGNED(bias, esize(wdtype));
+  REQUIRE_ELEM_ALIGNED(mean, sizeof(float));
+  REQUIRE_ELEM_ALIGNED(rstd, sizeof(float));
   return launch_layernorm_fwd(x, ldx, weight, bias, T, d, dtype, wdtype, eps, y, mean, rstd,
                               (cudaStream_t)stream);
 }
@@ -908,6 +910,10 @@ int moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   REQUIRE_ELEM_ALIGNED(addend, esize(dtype));
   REQUIRE_ELEM_ALIGNED(dx, esize(dtype));
   REQUIRE_ELEM_ALIGNED(weight, esize(wdtype));
+  REQUIRE_ELEM_ALIGNED(mean, sizeof(float));
+  REQUIRE_ELEM_ALIGNED(rstd, sizeof(float));
+  REQUIRE_ELEM_ALIGNED(dweight, sizeof(float));
+  REQUIRE_ELEM_ALIGNED(dbias, sizeof(float));
   if (dweight != nullptr || dbias != nullptr) {
     if (ws == nullptr || ws_bytes < layernorm_bwd_ws_bytes(T, d))
       return fail(MOE_ERR_WORKSPACE, "layernorm workspace smaller than moe_layernorm_bwd_workspace_size()");
@@ -951,9 +957,16 @@ static int check_ffn(int T, int d, int f, int dtype) {
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T must be >= 0");
   if (d <= 0 || d % 8) return fail(MOE_ERR_UNSUPPORTED, "d must be a positive multiple of 8");
   if (f <= 0 || f % 8) return fail(MOE_ERR_UNSUPPORTED, "f must be a positive multiple of 8");
-  const int64_t most = (int64_t)1 << 38;   // elements of a matrix: tile counts stay within 32 bits
-  if (T > (1 << 30) || (int64_t)T * d > most || (int64_t)T * f > most || (int64_t)d * f > most)
-    return fail(MOE_ERR_UNSUPPORTED, "T must be <= 2^30 and every matrix <= 2^38 elements");
+  // extents, tile counts and k-blocks stay within 32 bits
+  const int64_t most = (int64_t)1 << 38;
+  if (T > (1 << 30) || d > (1 << 28) || f > (1 << 28) || (int64_t)T * d > most ||
+      (int64_t)T * f > most || (int64_t)d * f > most)
+    return fail(MOE_ERR_UNSUPPORTED, "T must be <= 2^30, d and f <= 2^28, a matrix <= 2^38 elements");
+  return MOE_OK;
+}
+
+static int check_ffn_call(int T, int d, int f, int dtype) {
+  if (int rc = check_ffn(T, d, f, dtype)) return rc;
   if (!tc_available()) return fail(MOE_ERR_UNSUPPORTED, "the shared FFN needs an sm_100 device");
   return MOE_OK;
 }
@@ -969,7 +982,7 @@ size_t moe_shared_ffn_fwd_workspace_size(int T, int d, int f, int dtype) {
 int moe_shared_ffn_fwd(const void* x, const void* w1, const void* w3, const void* w2,
                        const void* addend, int T, int d, int f, int dtype, void* H, void* y,
                        void* ws, size_t ws_bytes, void* stream) {
-  if (int rc = check_ffn(T, d, f, dtype)) return rc;
+  if (int rc = check_ffn_call(T, d, f, dtype)) return rc;
   if (T == 0) return MOE_OK;
   REQUIRE_PTR(x); REQUIRE_PTR(w1); REQUIRE_PTR(w3); REQUIRE_PTR(w2); REQUIRE_PTR(y);
   REQUIRE_ALIGNED(x); REQUIRE_ALIGNED(w1); REQUIRE_ALIGNED(w3); REQUIRE_ALIGNED(w2);
@@ -997,7 +1010,7 @@ int moe_shared_ffn_bwd(const void* dout, const void* x, const void* w1, const vo
                        const void* w2, const void* H, const void* addend, int T, int d, int f,
                        int dtype, void* dx, void* dw1, void* dw3, void* dw2, void* ws,
                        size_t ws_bytes, void* stream) {
-  if (int rc = check_ffn(T, d, f, dtype)) return rc;
+  if (int rc = check_ffn_call(T, d, f, dtype)) return rc;
   REQUIRE_PTR(dw1); REQUIRE_PTR(dw3); REQUIRE_PTR(dw2);
   cudaStream_t s = (cudaStream_t)stream;
   if (T == 0) {   // no rows: the sums over them are zero

@@ -526,24 +526,6 @@ __device__ __forceinline__ void epi_barrier() {   // the epilogue warps
   asm volatile("bar.sync 1, %0;" ::"n"(EW * 32) : "memory");
 }
 
-// Columns 32 h .. of row `lane` of a box: 16-byte chunk c at chunk c ^ (lane & 7).
-__device__ __forceinline__ void box_get(const uint8_t* box, int lane, int h, uint4 (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p[i] = *reinterpret_cast<const uint4*>(box + lane * 128 + (((4 * h + i) ^ (lane & 7)) << 4));
-}
-__device__ __forceinline__ void box_put(uint8_t* box, int lane, int h, const float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 b[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-    uint4 u;
-    memcpy(&u, b, 16);
-    *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + i) ^ (lane & 7)) << 4)) = u;
-  }
-}
-
 // The walk of one pair over its work: whole tiles, then its share.
 struct FWalk {
   int u, step, lim;      // next whole tile

@@ -151,6 +151,8 @@ class MoEBlockStep:
         dtype = torch.bfloat16
         if layer.setdefault("dtype", dtype) != dtype:
             raise ValueError("MoEBlockStep is bf16 only")
+        if d % 8 or f_shared <= 0 or f_shared % 8:
+            raise ValueError("MoEBlockStep: d and f_shared must be positive multiples of 8")
         self.p, self.eps = p, eps
         self.moe = MoELayerStep(T, d, f, E, k, device=device, **layer)
         e = lambda *s, dt=dtype: torch.empty(*s, device=device, dtype=dt)  # noqa: E731

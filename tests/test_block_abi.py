@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from mixture_experts_layer_59_b200 import binding as B
+from mixture_experts_layer_59_b200.layer import MoEBlockStep
 
 F = ctypes.c_void_p(256)
 ODD = ctypes.c_void_p(257)
@@ -88,7 +89,7 @@ def ffn_bwd(**kw):
 
 
 SHARED = [(dict(dt=B.MOE_F32), -2), (dict(T=-1), -1), (dict(d=12), -2), (dict(f=4), -2), (dict(d=0), -2),
-          (dict(f=-8), -2), (dict(T=1 << 30, d=1 << 20), -2), (dict(d=1 << 20, f=1 << 20), -2), (dict(x=None), -1), (dict(w1=None), -1), (dict(w3=None), -1),
+          (dict(f=-8), -2), (dict(T=1 << 30, d=1 << 20), -2), (dict(d=1 << 20, f=1 << 20), -2), (dict(T=1, d=8, f=1 << 29), -2), (dict(x=None), -1), (dict(w1=None), -1), (dict(w3=None), -1),
           (dict(w2=None), -1), (dict(x=ctypes.c_void_p(264)), -1), (dict(w2=ctypes.c_void_p(258)), -1),
           (dict(add=ctypes.c_void_p(258)), -1), (dict(ws=None), -1), (dict(wsb=8), -5)]
 
@@ -131,3 +132,38 @@ def test_layernorm_workspace_covers_every_launch_shape():
     for d in (1, 33, 700, 1037, 4096, 8192):
         assert size(5, d) == 5 * 2 * d * 4 and size(100000, d) == 592 * 2 * d * 4
     assert size(1, 8193) == 64 * 2 * 8193 * 4
+
+
+def test_shared_ffn_workspace_holds_the_activation():
+    # the forward's A, the backward's dH and A, each [T, f] or [T, 2f] bf16 at 256-byte steps
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for T, d, f in ((1, 256, 128), (300, 72, 520), (16384, 2048, 1024)):
+        assert B.moe_shared_ffn_fwd_workspace_size(T, d, f) >= up(T * f * 2)
+        assert B.moe_shared_ffn_bwd_workspace_size(T, d, f) >= up(T * f * 4) + up(T * f * 2)
+
+
+def test_sizes_past_32_bits_are_refused():
+    # ctypes would wrap them; a meta tensor has the shape without the memory
+    for shape in ((1 << 32, 8), (8, 1 << 31)):
+        x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+        with pytest.raises(B.MoEError, match="2.31"):
+            B.moe_layernorm_fwd(x)
+
+
+def test_block_step_host_side():
+    T, d, f, E, k, fs = 300, 256, 128, 8, 2, 72
+    s = MoEBlockStep(T, d, f, E, k, fs, p=0.1, device="cpu", round_mode=B.MOE_ROUND_NONE)
+    assert s.moe.round_mode == B.MOE_ROUND_NONE and s.n.dtype == torch.bfloat16
+    assert tuple(s.Hs.shape) == (T, 2 * fs) and s.mean.dtype == torch.float32
+    assert s.ws_fwd.numel() == B.moe_shared_ffn_fwd_workspace_size(T, d, fs) > 0
+    assert s.ws_bwd.numel() == B.moe_shared_ffn_bwd_workspace_size(T, d, fs) > 0
+    assert s.ws_ln.numel() == B.moe_layernorm_bwd_workspace_size(T, d) > 0
+    assert tuple(s.ffn_grads["dw2"].shape) == (fs, d) and tuple(s.ln_grads["dbias"].shape) == (d,)
+    with pytest.raises(ValueError, match="bf16"):
+        MoEBlockStep(T, d, f, E, k, fs, device="cpu", dtype=torch.float32)
+    for bad in (0, -8, 12):
+        with pytest.raises(ValueError, match="multiples of 8"):
+            MoEBlockStep(T, d, f, E, k, bad, device="cpu")
+    x = torch.zeros(T, d, dtype=torch.bfloat16)
+    with pytest.raises(B.MoEError, match="CUDA device"):
+        s.forward(x, (None, None), (), (), torch.zeros(2, dtype=torch.int64))
