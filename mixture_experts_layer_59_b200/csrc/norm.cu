@@ -136,9 +136,12 @@ struct Vals {
   }
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum over the `lanes` (a power of two) neighbours that share a row; every
+// lane of the warp calls it.
+__device__ __forceinline__ float warp_sum(float v, int lanes = 32) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -159,16 +162,19 @@ constexpr int LN_SMS = 148;
 // ============================================================== forward
 // A group of WPR warps holds one row: NV packs of V elements per thread.
 // 16384 x 2048 bf16: 29 us, 4.6 TB/s (a plain copy of that size 25 us).
-template <class T, class W, int V, int NV, int WPR>
+// Narrow rows: LPR lanes to a row, several rows in a warp (200000 x 128: 29 us,
+// a warp to a row 59).
+template <class T, class W, int V, int NV, int WPR, int LPR = 32>
 __global__ void __launch_bounds__(WPR > 8 ? 1024 : 256)
 k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
          float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float inv_d, float eps) {
   __shared__ float red[2][32];
-  constexpr int wpr = WPR;
+  static_assert(LPR == 32 || WPR == 1, "a row lies in a part of a warp or in whole warps");
+  constexpr int wpr = WPR, G = WPR * LPR;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rpb = (blockDim.x >> 5) / wpr;
-  const int64_t row = (int64_t)blockIdx.x * rpb + warp / wpr;
-  const int lin = (warp % wpr) * 32 + lane, G = wpr * 32;
+  const int rpb = blockDim.x / G;
+  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / G;
+  const int lin = threadIdx.x % G;
   const bool live = row < T_;
   typedef Vals<T, V, NV> X;
   const F2 zero = f2(0.f, 0.f);
@@ -182,7 +188,10 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
     acc = f2_add(acc, v[m]);
   }
   const float2 a1 = f2_get(acc);
-  const float mu = group_sum(a1.x + a1.y, red[0], wpr, warp, lane) * inv_d;
+  auto sum = [&](float e, float* r) {
+    return LPR < 32 ? warp_sum(e, LPR) : group_sum(e, r, wpr, warp, lane);
+  };
+  const float mu = sum(a1.x + a1.y, red[0]) * inv_d;
   const F2 nmu = f2(-mu, -mu);
   acc = zero;
 #pragma unroll
@@ -197,7 +206,7 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
     acc = f2_fma(v[m], v[m], acc);
   }
   const float2 a2 = f2_get(acc);
-  const float rs = rsqrtf(group_sum(a2.x + a2.y, red[1], wpr, warp, lane) * inv_d + eps);
+  const float rs = rsqrtf(sum(a2.x + a2.y, red[1]) * inv_d + eps);
   if (!live) return;
   const F2 rs2 = f2(rs, rs);
   // the parameters pack by pack (of pairs of packs where V is 1): few registers
@@ -232,19 +241,21 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
 // move from row to row, so w and b lie in shared memory as fp32, V columns and
 // a word to spare: element k of unit j is word (V + 1) j - o + k, less one
 // where k < o (a choice that the whole row shares), and a warp's 32 units hit
-// 32 banks.  Persistent blocks of 8 warps, gw to a row.  32000 x 1037 bf16 in
+// 32 banks.  Persistent blocks of 8 warps, gw to a row (narrow
+// rows: lpr lanes).  32000 x 1037 bf16 in
 // 60 us; by single elements 129.
 template <class T, class W, int NV>
 __global__ void __launch_bounds__(256, 3)
 k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
                float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float inv_d,
-               float eps, int gw) {
+               float eps, int gw, int lpr) {
   extern __shared__ float params[];              // w, then b
   __shared__ float red[2][2][8];
   constexpr int V = 16 / (int)sizeof(T), HV = V / 2;
   typedef Vals<T, V, 1> P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = warp / gw, groups = 8 / gw, lin = (warp % gw) * 32 + lane, G = gw * 32;
+  const int grp = warp / gw, G = gw * lpr;        // lpr < 32: gw = 1
+  const int lin = (warp % gw) * 32 + lane % lpr, sub = lane / lpr, subs = 32 / lpr;
   float *sw = params, *sb = params + (d / V + 1) * (V + 1);
   for (int c = threadIdx.x; c < d; c += 256) {
     const int i = c / V * (V + 1) + c % V;
@@ -253,7 +264,7 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
   }
   __syncthreads();
   auto sum = [&](float v, float* r) {            // over the row's warps
-    v = warp_sum(v);
+    v = warp_sum(v, lpr);
     if (gw == 1) return v;
     if (lane == 0) r[warp] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(G) : "memory");
@@ -262,8 +273,11 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
     return v;
   };
   int odd = 0;
-  const int64_t rstep = (int64_t)gridDim.x * groups;
-  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < T_; row += rstep, odd ^= 1) {
+  const int rows = 8 / gw * subs;                // of a block at a time
+  for (int64_t r0 = (int64_t)blockIdx.x * rows + grp * subs; r0 < T_;
+       r0 += (int64_t)gridDim.x * rows, odd ^= 1) {
+    const int64_t row = r0 + sub;
+    const int dd = row < T_ ? d : 0;             // a row past the last has no columns
     const T* xr = x + row * ldx;
     const int o = (int)((reinterpret_cast<uintptr_t>(xr) & 15u) / sizeof(T));
     const T* xa = xr - o;                        // the row's first unit
@@ -271,9 +285,9 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
     P raw[NV];
     F2 v[NV * HV], acc = f2(0.f, 0.f);
     // column of element k of unit i: inside the row?
-    auto in = [&](int i, int k) { return (unsigned)((lin + i * G) * V - o + k) < (unsigned)d; };
+    auto in = [&](int i, int k) { return (unsigned)((lin + i * G) * V - o + k) < (unsigned)dd; };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) raw[i].load(xa, (lin + i * G) * V, 0, o + d);
+    for (int i = 0; i < NV; ++i) raw[i].load(xa, (lin + i * G) * V, 0, dd ? o + d : 0);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const bool whole = in(i, 0) && in(i, V - 1);
@@ -339,7 +353,7 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
           }
       }
     }
-    if (lin == 0 && mean) {
+    if (lin == 0 && dd && mean) {
       mean[row] = mu;
       rstd[row] = rs;
     }
@@ -380,11 +394,11 @@ k_ln_fwd_wide(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restr
 
 // ============================================================== backward
 // Any rows of up to 8192 columns.  A block walks rows; a group of G threads
-// owns a row at a time and each thread the same 8 columns of every row, so
-// that the column sums of dy xh and dy stay in registers until the block's
-// last row and leave as one partial row per block.
+// (whole warps, or 4, 8 or 16 lanes) owns a row at a time and each thread the
+// same 8 columns of every row, so that the column sums of dy xh and dy stay in
+// registers until the block's last row and leave as one partial row per block.
 template <class T, class W, int V, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 512 / MAXT : 1)
+__global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : (V > 1 && MAXT == 128 ? 6 : 512 / MAXT))
 k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
          const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
          int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, float inv_d, int G) {
@@ -431,13 +445,20 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
       }
     }
     const float2 p1 = f2_get(t1), p2 = f2_get(t2);
-    // both sums over the warp: each half goes on with one
-    const bool hi = lane & 16;
     const float u1 = p1.x + p1.y, u2 = p2.x + p2.y;
-    float u = (hi ? u2 : u1) + __shfl_xor_sync(0xffffffffu, hi ? u1 : u2, 16);
+    float s1, s2;
+    if (G < 32) {
+      s1 = warp_sum(u1, G);
+      s2 = warp_sum(u2, G);
+    } else {
+      // both sums over the warp: each half goes on with one
+      const bool hi = lane & 16;
+      float u = (hi ? u2 : u1) + __shfl_xor_sync(0xffffffffu, hi ? u1 : u2, 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    float s1 = __shfl_sync(0xffffffffu, u, 0), s2 = __shfl_sync(0xffffffffu, u, 16);
+      for (int o = 8; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      s1 = __shfl_sync(0xffffffffu, u, 0);
+      s2 = __shfl_sync(0xffffffffu, u, 16);
+    }
     if (wpg > 1) {                         // two buffers: one barrier per row
       if (lane == 0) red[it & 1][warp] = make_float2(s1, s2);
       __syncthreads();
@@ -466,10 +487,21 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
     vx.store(dx + row * d, col, step, dd);
   }
   if (part == nullptr) return;
-  // the groups' sums, added in order
+  // the groups' sums, added in order: those of a warp by shuffles first
+  if (G < 32)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o >= G)
+#pragma unroll
+        for (int m = 0; m < X::NP; ++m) {
+          aw[m].v = f2_add(aw[m], F2{__shfl_xor_sync(0xffffffffu, aw[m].v, o)}).v;
+          ab[m].v = f2_add(ab[m], F2{__shfl_xor_sync(0xffffffffu, ab[m].v, o)}).v;
+        }
+  const int owners = G < 32 ? (int)blockDim.x / 32 : groups;
+  const int own = G < 32 ? (lane < G ? warp : -1) : grp;
   float* pr = part + (size_t)blockIdx.x * 2 * d;
-  for (int k = 0; k < groups; ++k) {
-    if (grp == k) {
+  for (int k = 0; k < owners; ++k) {
+    if (own == k) {
 #pragma unroll
       for (int m = 0; m < X::NP; ++m) {
         const float2 sw = f2_get(aw[m]), sb = f2_get(ab[m]);
@@ -482,14 +514,14 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
               u += colsum[c];
               v += colsum[d + c];
             }
-            float* to = k == groups - 1 ? pr : colsum;
+            float* to = k == owners - 1 ? pr : colsum;
             to[c] = u;
             to[d + c] = v;
           }
         }
       }
     }
-    if (groups > 1) __syncthreads();
+    if (owners > 1) __syncthreads();
   }
 }
 
@@ -823,6 +855,20 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
   const int nv = (npack + wpr * 32 - 1) / (wpr * 32);
   const float inv_d = 1.0f / (float)d;
   ProfScope _ps("layernorm_fwd", s);
+  if constexpr (V * sizeof(T) == 16) {
+    // two packs per lane fill at most half a warp: 4, 8 or 16 lanes to a row
+    if (npack <= 32 && T_ > LN_SMS * 16) {
+#define LN_GO(LPR)                                                                            \
+  k_ln_fwd<T, W, V, 2, 1, LPR><<<(T_ + (int64_t)(256 / LPR) - 1) / (256 / LPR), 256, 0, s>>>( \
+      x, ldx, w, b, y, mean, rstd, T_, d, inv_d, eps)
+      if (npack <= 8) LN_GO(4);
+      else if (npack <= 16) LN_GO(8);
+      else LN_GO(16);
+#undef LN_GO
+      MOE_CHECK_LAUNCH("layernorm_fwd");
+      return MOE_OK;
+    }
+  }
 #define LN_GO(NV, WPR)                                                                        \
   do {                                                                                        \
     const int rpb = WPR == 1 ? 2 : 1;   /* rows per block */                                  \
@@ -865,7 +911,10 @@ int ln_fwd_units(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d,
   if (units > gw * 32 * MAXNV || (int64_t)T_ * gw < LN_SMS * 8) return 1;
   const size_t bytes = (size_t)2 * (d / V + 1) * (V + 1) * sizeof(float);
   const int per_sm = (int)std::min<size_t>(216 * 1024 / bytes, 3);
-  const int64_t want = ((int64_t)T_ * gw + 7) / 8;
+  int lpr = 32;                                  // the fewest lanes that hold a narrow row
+  while (lpr > 4 && units * 2 <= lpr * (MAXNV * 2 / 5)) lpr /= 2;
+  const int rows = 8 / gw * (32 / lpr);          // of a block at a time
+  const int64_t want = ((int64_t)T_ + rows - 1) / rows;
   const int grid = (int)std::min<int64_t>(want, LN_SMS * per_sm);
   ProfScope _ps("layernorm_fwd", s);
 #define LN_GO(NV)                                                                              \
@@ -873,9 +922,9 @@ int ln_fwd_units(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d,
     if (cudaError_t e = smem_limit<k_ln_fwd_units<T, W, NV>>(100 * 1024))                      \
       return cuda_fail(e, "layernorm smem attribute");                                         \
     k_ln_fwd_units<T, W, NV><<<grid, 256, bytes, s>>>(x, ldx, w, b, y, mean, rstd, T_, d,      \
-                                                      1.0f / (float)d, eps, gw);               \
+                                                      1.0f / (float)d, eps, gw, lpr);          \
   } while (0)
-  const int nv = (units + gw * 32 - 1) / (gw * 32);
+  const int nv = (units + gw * lpr - 1) / (gw * lpr);
   if (nv * 5 <= MAXNV * 2) LN_GO(MAXNV * 2 / 5);
   else if (nv * 5 <= MAXNV * 3) LN_GO(MAXNV * 3 / 5);
   else if (nv * 5 <= MAXNV * 4) LN_GO(MAXNV * 4 / 5);
@@ -906,7 +955,11 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
 }
 
 constexpr int LN_COLS = 8192;     // widest row of k_ln_bwd: 8 columns x 1024 threads
-constexpr int LN_PARTS = LN_SMS * 4;   // most blocks of either kernel
+constexpr int LN_PARTS = LN_SMS * 6;   // most blocks of either kernel
+// Columns up to which k_ln_bwd takes many rows as well: a stage of k_ln_bwd_ws
+// is too few bytes there (200000 rows of 128 bf16: 57 us against 134 by
+// k_ln_bwd_ws; of 256: 97 and 138; 100000 of 512: 130 and 95).
+constexpr int LN_NARROW = 256;
 constexpr int LN_SLICES = 64;     // row slices of k_ln_bwd_cols
 // Launch shape of k_ln_bwd_ws for packs of v; R = 0 where rows are too wide or
 // too few to give every block a few stages.
@@ -976,15 +1029,20 @@ int ln_bwd_v(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, con
              int* nparts, cudaStream_t s) {
   if constexpr (V * sizeof(T) == 16 || V == 1) {
     const LnWs p = ln_bwd_ws(T_, d, sizeof(T), V, add != nullptr);
-    if (p.R) {
+    if (p.R && d > LN_NARROW) {
       *nparts = p.grid;
       return ln_bwd_ws_go<T, W, V>(p, dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T_, d, dx, part, s);
     }
   }
-  const int G = ((d + 7) / 8 + 31) / 32 * 32, groups = G >= 128 ? 1 : 128 / G, block = G * groups;
+  // threads of a row: whole warps, or a power of two below
+  int G = ((d + 7) / 8 + 31) / 32 * 32;
+  while (G <= 32 && G > 4 && d <= G * 4) G /= 2;
+  const int groups = G >= 128 ? 1 : 128 / G, block = G * groups;
   const size_t smem = groups > 1 ? (size_t)2 * d * sizeof(float) : 0;
   const int64_t steps = ((int64_t)T_ + groups - 1) / groups;
-  const int per_sm = std::min(4, block <= 512 ? 512 / block : 1);   // LN_PARTS allows for 4
+  // 200000 x 128 bf16: 6 blocks of 128 threads per SM 57 us, 4 69; by single
+  // elements (V = 1) 6 cost registers, 200000 x 127: 119 and 101
+  const int per_sm = block > 512 ? 1 : (V > 1 && G <= 32 ? 6 : std::min(4, 512 / block));
   const int grid = (int)std::min<int64_t>(steps, LN_SMS * per_sm);
   *nparts = grid;
   ProfScope _ps("layernorm_bwd", s);
@@ -1025,7 +1083,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
   return ln_bwd_v<T, W, V>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, T_, d, dxt, part, nparts, s)
   if constexpr (sizeof(T) == 2) {
     if (v == 8) LN_V(8);
-    if (v == 2 && ln_bwd_ws(T_, d, 2, 1, add != nullptr).R == 0) LN_V(2);
+    if (v == 2 && (d <= LN_NARROW || ln_bwd_ws(T_, d, 2, 1, add != nullptr).R == 0)) LN_V(2);
   } else {
     if (v == 4) LN_V(4);
   }

@@ -9,7 +9,7 @@ output type, finfo(t).eps / 2 (fp32 2^-24, bf16 2^-8).
    Each result then takes a handful of further roundings: 256 u times the
    sum of the magnitudes of its terms bounds them all, plus h times the
    result for the last rounding.
- - dweight, dbias: a thread adds at most T / 64 rows, then at most 592 / 32
+ - dweight, dbias: a thread adds at most T / 64 rows, then at most 888 / 32
    partial rows and 32 column slices; with T <= 4000 fewer than 128
    roundings: 256 u times the sum of the terms' magnitudes.
  - dropout: the scale, the product and the sum round once each: 4 u times the
@@ -95,6 +95,16 @@ def test_layernorm(T, d, dtype, wdtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [1, 2, 3, 8, 15, 16, 17, 31, 32, 40, 63, 64, 72, 100, 128, 129, 130, 200, 255, 256])
+def test_layernorm_many_narrow_rows(d, dtype):
+    """Rows of less than a warp's width, several to a warp; the last warp not full."""
+    gen = torch.Generator().manual_seed(d)
+    for T in (2369, 4099):
+        x, dy = draw(gen, T, d, dtype=dtype, std=2.0, mean=0.5), draw(gen, T, d, dtype=dtype)
+        check_ln(x, draw(gen, d, std=0.2, mean=1.0), draw(gen, d), dy=dy, add=draw(gen, T, d, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("w,b", [(False, False), (True, False), (False, True)])
 def test_layernorm_without_weight_or_bias(dtype, w, b):
     gen = torch.Generator().manual_seed(5)
@@ -114,7 +124,8 @@ def test_layernorm_row_strides_and_alignment(dtype, d, pad, skip):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T,d,pad,skip", [(9600, 128, 3, 1), (3000, 1000, 8, 4), (3000, 1001, 8, 3), (3000, 1001, 5, 0)])
+@pytest.mark.parametrize("T,d,pad,skip", [(9600, 128, 3, 1), (9601, 128, 8, 8), (5001, 16, 8, 0), (5001, 33, 5, 2),
+                                          (4003, 200, 8, 4), (3000, 1000, 8, 4), (3000, 1001, 8, 3), (3000, 1001, 5, 0)])
 def test_layernorm_many_rows_inside_a_wider_matrix(T, d, pad, skip, dtype):
     """Each array at an offset of its own, NaN all around the rows."""
     gen = torch.Generator().manual_seed(T + d + pad + skip)
