@@ -234,28 +234,29 @@ k_ln_fwd(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__
   }
 }
 
-// Many rows that do not start at 16-byte units, x and y alike.  Each row is
+// Many wide bf16 rows that do not start at 4-byte units, x and y alike.  Each row is
 // walked in the 16-byte units that hold it: unit j holds columns V j - o ..,
 // o the row's offset in its first unit; columns outside the row count as
 // nothing, and whole units leave as one store.  The columns of a thread thus
 // move from row to row, so w and b lie in shared memory as fp32, V columns and
 // a word to spare: element k of unit j is word (V + 1) j - o + k, less one
 // where k < o (a choice that the whole row shares), and a warp's 32 units hit
-// 32 banks.  Persistent blocks of 8 warps, gw to a row (narrow
-// rows: lpr lanes).  32000 x 1037 bf16 in
-// 60 us; by single elements 129.
-template <class T, class W, int NV>
+// 32 banks.  Persistent blocks of 8 warps, gw to a row.  9563 x 7017 in 107 us
+// (by single elements 178), 32000 x 1037 in 63 (76); narrower rows and fp32 ones
+// are faster by single elements, which need no shared memory: 60000 x 767 in
+// 68 (84), 32000 x 1037 fp32 in 53 (76).
+template <class W, int NV>
 __global__ void __launch_bounds__(256, 3)
-k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
-               float* __restrict__ mean, float* __restrict__ rstd, int T_, int d, float inv_d,
-               float eps, int gw, int lpr) {
+k_ln_fwd_units(const __nv_bfloat16* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b,
+               __nv_bfloat16* y, float* __restrict__ mean, float* __restrict__ rstd, int T_,
+               int d, float inv_d, float eps, int gw) {
   extern __shared__ float params[];              // w, then b
   __shared__ float red[2][2][8];
-  constexpr int V = 16 / (int)sizeof(T), HV = V / 2;
+  typedef __nv_bfloat16 T;
+  constexpr int V = 8, HV = V / 2;
   typedef Vals<T, V, 1> P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = warp / gw, G = gw * lpr;        // lpr < 32: gw = 1
-  const int lin = (warp % gw) * 32 + lane % lpr, sub = lane / lpr, subs = 32 / lpr;
+  const int grp = warp / gw, groups = 8 / gw, lin = (warp % gw) * 32 + lane, G = gw * 32;
   float *sw = params, *sb = params + (d / V + 1) * (V + 1);
   for (int c = threadIdx.x; c < d; c += 256) {
     const int i = c / V * (V + 1) + c % V;
@@ -264,7 +265,7 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
   }
   __syncthreads();
   auto sum = [&](float v, float* r) {            // over the row's warps
-    v = warp_sum(v, lpr);
+    v = warp_sum(v);
     if (gw == 1) return v;
     if (lane == 0) r[warp] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(G) : "memory");
@@ -273,11 +274,8 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
     return v;
   };
   int odd = 0;
-  const int rows = 8 / gw * subs;                // of a block at a time
-  for (int64_t r0 = (int64_t)blockIdx.x * rows + grp * subs; r0 < T_;
-       r0 += (int64_t)gridDim.x * rows, odd ^= 1) {
-    const int64_t row = r0 + sub;
-    const int dd = row < T_ ? d : 0;             // a row past the last has no columns
+  const int64_t rstep = (int64_t)gridDim.x * groups;
+  for (int64_t row = (int64_t)blockIdx.x * groups + grp; row < T_; row += rstep, odd ^= 1) {
     const T* xr = x + row * ldx;
     const int o = (int)((reinterpret_cast<uintptr_t>(xr) & 15u) / sizeof(T));
     const T* xa = xr - o;                        // the row's first unit
@@ -285,9 +283,9 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
     P raw[NV];
     F2 v[NV * HV], acc = f2(0.f, 0.f);
     // column of element k of unit i: inside the row?
-    auto in = [&](int i, int k) { return (unsigned)((lin + i * G) * V - o + k) < (unsigned)dd; };
+    auto in = [&](int i, int k) { return (unsigned)((lin + i * G) * V - o + k) < (unsigned)d; };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) raw[i].load(xa, (lin + i * G) * V, 0, dd ? o + d : 0);
+    for (int i = 0; i < NV; ++i) raw[i].load(xa, (lin + i * G) * V, 0, o + d);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const bool whole = in(i, 0) && in(i, V - 1);
@@ -353,7 +351,7 @@ k_ln_fwd_units(const T* x, int64_t ldx, const W* __restrict__ w, const W* __rest
           }
       }
     }
-    if (lin == 0 && dd && mean) {
+    if (lin == 0 && mean) {
       mean[row] = mu;
       rstd[row] = rs;
     }
@@ -846,24 +844,29 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
              float* mean, float* rstd, cudaStream_t s) {
   const int npack = d / V;
   // Warps per row: as few as hold the row in 32 columns a thread (16384 x 2048
-  // bf16: 2 warps 36 us, 1 warp with 64 columns 44, 4 warps 38); more while
-  // the rows alone do not give the SMs 16 warps each (few rows: latency).
-  constexpr int PT = V * sizeof(T) == 16 ? 32 / V : 4;
+  // bf16: 2 warps 36 us, 1 warp with 64 columns 44, 4 warps 38), in 12 by
+  // single fp32 elements (8: 32000 x 1037 80 us, 12: 53), 8 by bf16 ones (60000
+  // x 767: 68 us, 12: 104); more while the rows alone do not give the SMs 16
+  // warps each (few rows: latency).
+  constexpr int PT = V * sizeof(T) == 16 ? 32 / V : (V == 1 && sizeof(T) == 4 ? 12 : 8);
   int wpr = 1;
   while (wpr < 32 && npack > wpr * 32 * PT) wpr *= 2;
   while (wpr < 32 && npack > wpr * 32 && (int64_t)T_ * wpr < LN_SMS * 16) wpr *= 2;
   const int nv = (npack + wpr * 32 - 1) / (wpr * 32);
   const float inv_d = 1.0f / (float)d;
   ProfScope _ps("layernorm_fwd", s);
-  if constexpr (V * sizeof(T) == 16) {
-    // two packs per lane fill at most half a warp: 4, 8 or 16 lanes to a row
-    if (npack <= 32 && T_ > LN_SMS * 16) {
-#define LN_GO(LPR)                                                                            \
-  k_ln_fwd<T, W, V, 2, 1, LPR><<<(T_ + (int64_t)(256 / LPR) - 1) / (256 / LPR), 256, 0, s>>>( \
+  {
+    // A row in a warp or a part of it, 256 threads to a block: two packs of
+    // 16 bytes (four of 4) per lane, or 8 single elements (200000 x 127 bf16: 37 us, 94 by units).
+    constexpr int PL = V == 1 ? 8 : (V * sizeof(T) == 16 ? 2 : 4);
+    if (npack <= 32 * PL && T_ > LN_SMS * 16) {
+#define LN_GO(LPR)                                                                             \
+  k_ln_fwd<T, W, V, PL, 1, LPR><<<(T_ + (int64_t)(256 / LPR) - 1) / (256 / LPR), 256, 0, s>>>( \
       x, ldx, w, b, y, mean, rstd, T_, d, inv_d, eps)
-      if (npack <= 8) LN_GO(4);
-      else if (npack <= 16) LN_GO(8);
-      else LN_GO(16);
+      if (npack <= 4 * PL) LN_GO(4);
+      else if (npack <= 8 * PL) LN_GO(8);
+      else if (npack <= 16 * PL) LN_GO(16);
+      else LN_GO(32);
 #undef LN_GO
       MOE_CHECK_LAUNCH("layernorm_fwd");
       return MOE_OK;
@@ -884,13 +887,18 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
     else if (wpr == 16) LN_GO(NV, 16);                                                        \
     else LN_GO(NV, 32);                                                                       \
   } while (0)
-  if (nv > 8) k_ln_fwd_wide<T, W><<<T_, 1024, 0, s>>>(x, ldx, w, b, y, mean, rstd, d, eps);
-  else if (nv > 4) {
-    if constexpr (PT == 8) LN_W(8);
-    else LN_GO(8, 32);
+  if (nv > PT) k_ln_fwd_wide<T, W><<<T_, 1024, 0, s>>>(x, ldx, w, b, y, mean, rstd, d, eps);
+  else if (nv <= 2) LN_W(2);
+  else if (nv <= 4) LN_W(4);
+  else if constexpr (PT == 8 && V * sizeof(T) == 16) LN_W(8);
+  else if constexpr (PT > 4) {
+    if (nv <= 6) LN_W(6);
+    else if (nv <= 8) LN_W(8);
+    else if constexpr (PT > 8) {
+      if (nv <= 10) LN_W(10);
+      else LN_W(12);
+    }
   }
-  else if (nv > 2) LN_W(4);
-  else LN_W(2);
 #undef LN_W
 #undef LN_GO
   MOE_CHECK_LAUNCH("layernorm_fwd");
@@ -898,10 +906,11 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
 }
 
 // k_ln_fwd_units' launch; 1 where it does not fit or there are too few rows.
-template <class T, class W>
-int ln_fwd_units(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, float eps, T* y,
-                 float* mean, float* rstd, cudaStream_t s) {
-  constexpr int V = 16 / (int)sizeof(T), MAXNV = 40 / V;   // up to 40 columns per thread
+constexpr int LN_UNITS = 1024;    // columns from which it is the faster one
+template <class W>
+int ln_fwd_units(const __nv_bfloat16* x, int64_t ldx, const W* w, const W* b, int T_, int d,
+                 float eps, __nv_bfloat16* y, float* mean, float* rstd, cudaStream_t s) {
+  constexpr int V = 8, MAXNV = 5;                // up to 40 columns per thread
   if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15u) ||
       (ldx - d) % V)
     return 1;
@@ -911,24 +920,20 @@ int ln_fwd_units(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d,
   if (units > gw * 32 * MAXNV || (int64_t)T_ * gw < LN_SMS * 8) return 1;
   const size_t bytes = (size_t)2 * (d / V + 1) * (V + 1) * sizeof(float);
   const int per_sm = (int)std::min<size_t>(216 * 1024 / bytes, 3);
-  int lpr = 32;                                  // the fewest lanes that hold a narrow row
-  while (lpr > 4 && units * 2 <= lpr * (MAXNV * 2 / 5)) lpr /= 2;
-  const int rows = 8 / gw * (32 / lpr);          // of a block at a time
-  const int64_t want = ((int64_t)T_ + rows - 1) / rows;
+  const int64_t want = ((int64_t)T_ * gw + 7) / 8;
   const int grid = (int)std::min<int64_t>(want, LN_SMS * per_sm);
   ProfScope _ps("layernorm_fwd", s);
 #define LN_GO(NV)                                                                              \
   do {                                                                                         \
-    if (cudaError_t e = smem_limit<k_ln_fwd_units<T, W, NV>>(100 * 1024))                      \
+    if (cudaError_t e = smem_limit<k_ln_fwd_units<W, NV>>(100 * 1024))                         \
       return cuda_fail(e, "layernorm smem attribute");                                         \
-    k_ln_fwd_units<T, W, NV><<<grid, 256, bytes, s>>>(x, ldx, w, b, y, mean, rstd, T_, d,      \
-                                                      1.0f / (float)d, eps, gw, lpr);          \
+    k_ln_fwd_units<W, NV><<<grid, 256, bytes, s>>>(x, ldx, w, b, y, mean, rstd, T_, d,         \
+                                                   1.0f / (float)d, eps, gw);                  \
   } while (0)
-  const int nv = (units + gw * lpr - 1) / (gw * lpr);
-  if (nv * 5 <= MAXNV * 2) LN_GO(MAXNV * 2 / 5);
-  else if (nv * 5 <= MAXNV * 3) LN_GO(MAXNV * 3 / 5);
-  else if (nv * 5 <= MAXNV * 4) LN_GO(MAXNV * 4 / 5);
-  else LN_GO(MAXNV);
+  const int nv = (units + gw * 32 - 1) / (gw * 32);
+  if (nv <= 3) LN_GO(3);
+  else if (nv <= 4) LN_GO(4);
+  else LN_GO(5);
 #undef LN_GO
   MOE_CHECK_LAUNCH("layernorm_fwd");
   return MOE_OK;
@@ -941,11 +946,11 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
   const W *wt = (const W*)w, *bt = (const W*)b;
   T* yt = (T*)y;
   const int v = pick_pack<T, W>(d, {ldx}, {x, y}, {w, b});
-  if (v * (int)sizeof(T) < 16) {
-    const int rc = ln_fwd_units<T, W>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
-    if (rc <= 0) return rc;
-  }
   if constexpr (sizeof(T) == 2) {
+    if (v == 1 && d > LN_UNITS) {
+      const int rc = ln_fwd_units<W>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
+      if (rc <= 0) return rc;
+    }
     if (v == 8) return ln_fwd_v<T, W, 8>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
     if (v == 2) return ln_fwd_v<T, W, 2>(xt, ldx, wt, bt, T_, d, eps, yt, mean, rstd, s);
   } else {
@@ -955,11 +960,12 @@ int ln_fwd_t(const void* x, int64_t ldx, const void* w, const void* b, int T_, i
 }
 
 constexpr int LN_COLS = 8192;     // widest row of k_ln_bwd: 8 columns x 1024 threads
-constexpr int LN_PARTS = LN_SMS * 6;   // most blocks of either kernel
 // Columns up to which k_ln_bwd takes many rows as well: a stage of k_ln_bwd_ws
 // is too few bytes there (200000 rows of 128 bf16: 57 us against 134 by
 // k_ln_bwd_ws; of 256: 97 and 138; 100000 of 512: 130 and 95).
 constexpr int LN_NARROW = 256;
+// Most blocks of either kernel.
+int ln_blocks(int d) { return LN_SMS * (d <= LN_NARROW ? 6 : 4); }
 constexpr int LN_SLICES = 64;     // row slices of k_ln_bwd_cols
 // Launch shape of k_ln_bwd_ws for packs of v; R = 0 where rows are too wide or
 // too few to give every block a few stages.
@@ -1091,7 +1097,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
 #undef LN_V
 }
 
-int ln_parts(int T_, int d) { return d > LN_COLS ? LN_SLICES : std::min(T_, LN_PARTS); }
+int ln_parts(int T_, int d) { return d > LN_COLS ? LN_SLICES : std::min(T_, ln_blocks(d)); }
 
 }  // namespace
 

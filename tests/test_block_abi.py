@@ -126,11 +126,12 @@ def test_binding_refuses_ffn_arguments():
 
 
 def test_layernorm_workspace_covers_every_launch_shape():
-    # one partial row of 2 d floats per block, 888 blocks at most (8192 columns)
+    # one partial row of 2 d floats per block: 4 blocks per SM, 6 for narrow rows
     size = B.lib().moe_layernorm_bwd_workspace_size
     assert size(0, 700) == 0
-    for d in (1, 33, 700, 1037, 4096, 8192):
-        assert size(5, d) == 5 * 2 * d * 4 and size(100000, d) == 888 * 2 * d * 4
+    for d in (1, 33, 256, 257, 700, 1037, 4096, 8192):
+        assert size(5, d) == 5 * 2 * d * 4
+        assert size(100000, d) == (888 if d <= 256 else 592) * 2 * d * 4
     assert size(1, 8193) == 64 * 2 * 8193 * 4
 
 
