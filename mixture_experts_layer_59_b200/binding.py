@@ -525,6 +525,7 @@ def moe_token_bwd(dX_rows, dS, x, w_gate, idx, gate, plan, router_grad=True, gat
 # MoEError before anything is launched.
 _CODES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 _F32 = torch.float32
+_I32_MAX = 0x7fffffff
 
 
 def _bad(msg, code=MOE_ERR_INVALID_ARG):
@@ -535,9 +536,10 @@ def _matrix(name, t):
     """(rows, columns, dtype code) of a matrix of a supported dtype."""
     if t.dim() != 2:
         _bad(f"{name}: expected a matrix, got {t.dim()} dimensions")
-    if max(t.shape) > 0x7fffffff:
-        _bad(f"{name}: {tuple(t.shape)} has more than 2^31 - 1 rows or columns", MOE_ERR_UNSUPPORTED)
-    return (*t.shape, _code(name, t))
+    rows, cols = t.shape
+    if rows > _I32_MAX or cols > _I32_MAX:   # ctypes would wrap them
+        _bad(f"{name}: {rows} x {cols} has more than 2^31 - 1 rows or columns", MOE_ERR_UNSUPPORTED)
+    return rows, cols, _code(name, t)
 
 
 def _code(name, t):
@@ -591,12 +593,22 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(o, name, shape, like, dtype):
+def _out(o, name, like):
+    """The given output, or a new one, contiguous with like's shape and dtype."""
     t = o.get(name)
-    if t is None:
-        t = o[name] = like.new_empty(shape, dtype=dtype)
+    if t is not None:
+        _arg(name, t, like.shape, like.dtype, like.device)
+    else:   # empty_like is the fastest of torch's allocations
+        t = o[name] = torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
+    return t.data_ptr()
+
+
+def _out_f32(o, name, n, like):
+    t = o.get(name)
+    if t is not None:
+        _arg(name, t, (n,), _F32, like.device)
     else:
-        _arg(name, t, shape, dtype, like.device)
+        t = o[name] = like.new_empty(n, dtype=_F32)
     return t.data_ptr()
 
 
@@ -631,11 +643,12 @@ def moe_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rs
         with _there(x, stream):
             return moe_layernorm_fwd(x, weight, bias, eps, y, mean, rstd)
     if y is None:
-        y = x.new_empty((T, d))
+        y = torch.empty_like(x) if ldx == d else x.new_empty((T, d))
     else:
         _arg("y", y, (T, d), x.dtype, dev)
     if mean is None:
-        mean, rstd = x.new_empty(T, dtype=_F32), x.new_empty(T, dtype=_F32)
+        mean = x.new_empty(T, dtype=_F32)
+        rstd = torch.empty_like(mean)
     else:
         _arg("mean", mean, (T,), _F32, dev)
         _arg("rstd", rstd, (T,), _F32, dev)
@@ -667,8 +680,7 @@ def moe_layernorm_bwd(dy, x, weight, mean, rstd, addend=None, out=None, ws=None,
         with _there(x, stream):
             return moe_layernorm_bwd(dy, x, weight, mean, rstd, addend, out, ws)
     o = dict(out) if out else {}
-    dx = _out(o, "dx", (T, d), x, x.dtype)
-    dw, db = _out(o, "dweight", (d,), x, _F32), _out(o, "dbias", (d,), x, _F32)
+    dx, dw, db = _out(o, "dx", x), _out_f32(o, "dweight", d, x), _out_f32(o, "dbias", d, x)
     ws = _ws(ws, lib().moe_layernorm_bwd_workspace_size(T, d), x)
     _check(lib().moe_layernorm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, _ptr(weight),
                                    mean.data_ptr(), rstd.data_ptr(), _ptr(addend), ldadd, T, d, dt,
@@ -772,9 +784,8 @@ def moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend=None, out=None, ws=None, s
         with _there(x, stream):
             return moe_shared_ffn_bwd(dout, x, w1, w3, w2, H, addend, out, ws)
     o = dict(out) if out else {}
-    dx = _out(o, "dx", (T, d), x, x.dtype)
-    dw1, dw3 = _out(o, "dw1", (d, f), x, x.dtype), _out(o, "dw3", (d, f), x, x.dtype)
-    dw2 = _out(o, "dw2", (f, d), x, x.dtype)
+    dx, dw2 = _out(o, "dx", x), _out(o, "dw2", w2)
+    dw1, dw3 = _out(o, "dw1", w1), _out(o, "dw3", w3)
     ws = _ws(ws, lib().moe_shared_ffn_bwd_workspace_size(T, d, f, dt), x)
     _check(lib().moe_shared_ffn_bwd(dout.data_ptr(), x.data_ptr(), w1.data_ptr(), w3.data_ptr(),
                                     w2.data_ptr(), H.data_ptr(), _ptr(addend), T, d, f, dt, dx,
