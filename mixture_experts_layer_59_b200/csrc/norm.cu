@@ -532,15 +532,20 @@ k_ln_bwd(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict
 // us at 32768 x 1536 bf16 with an addend; with all 8 warps first at the rows'
 // sums, then at the columns, 87; this one 74 and 4 for the partial rows' sums:
 // 5.4 TB/s; a plain sum of two such tensors runs at 6.5.)
-// Rows that do not start and end at 16-byte units (V = 1) come with the bytes
-// around them (never another 16-byte unit than one that holds a byte of the
-// row) and are read from shared memory element by element, neighbouring
-// threads neighbouring columns.
+// Rows that do not start and end at 16-byte units come with the bytes around
+// them (never another 16-byte unit than one that holds a byte of the row) and
+// are read from shared memory in pairs (V = 2, rows at 4-byte units: 16000 x
+// 2046 66 us) or by single elements (x 2047: 82), neighbouring threads
+// neighbouring columns.
 constexpr int LN_STAGES = 6;                     // at most
 // Row-sum warps: with 16 column warps three, so that 20 warps leave each
-// thread 96 registers; single bf16 elements need more of them (9563 x 7017:
-// 212 us with 7, 280 with 3; fp32 loses by it, 6000 x 4341: 140 and 113).
-constexpr int ln_sum_warps(int cw, int v, int es) { return cw == 16 ? (v == 1 && es == 2 ? 7 : 3) : 4; }
+// thread 96 registers; bf16 in accesses of less than 16 bytes needs more of
+// them (9563 x 7017: 212 us with 7, 280 with 3; 12000 x 3002: 68 and 103; fp32
+// loses by it, 6000 x 4341: 140 and 113).  With 8 column warps four (32000 x
+// 1038 bf16: 84 us, with 6 102).
+constexpr int ln_sum_warps(int cw, int v, int es) {
+  return cw < 16 ? 4 : (es == 2 && v < 8 ? 7 : 3);
+}
 constexpr int ln_ws_threads(int cw, int v, int es) { return 32 * (cw + ln_sum_warps(cw, v, es) + 1); }
 
 template <class T, class W, int V, int E, int CW>
@@ -560,7 +565,8 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
   constexpr int NG = E / (V * PG), GP = P::NP;   // groups of packs per thread, pairs in one
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rb = (uint32_t)d * sizeof(T);
-  const uint32_t slot = V == 1 ? (rb + 15) / 16 * 16 + 16 : rb;   // a row's bytes in a stage
+  constexpr bool UNITS = V * sizeof(T) == 16;    // rows start and end at 16-byte units
+  const uint32_t slot = UNITS ? rb : (rb + 15) / 16 * 16 + 16;   // a row's bytes in a stage
   const int na = add ? 3 : 2;
   const uint32_t stage_bytes = (uint32_t)(na * R) * slot;
   const int64_t tiles = ((int64_t)T_ + R - 1) / R;
@@ -582,14 +588,14 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
   auto rows_of = [&](int64_t t) { return (int)(T_ - t * R < R ? T_ - t * R : R); };
   // where row r of array `arr` of the current stage begins (its source: p)
   auto in_stage = [&](int arr, int r, const T* p) {
-    const uint32_t off = V == 1 ? (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u : 0u;
+    const uint32_t off = UNITS ? 0u : (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
     return reinterpret_cast<const T*>(smem + (size_t)st * stage_bytes + (size_t)(arr * R + r) * slot + off);
   };
   if (warp == CW + SW) {
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       auto bytes_of = [&](const T* p) {
-        return V == 1 ? (((uint32_t)reinterpret_cast<uintptr_t>(p) & 15u) + rb + 15) / 16 * 16 : rb;
+        return UNITS ? rb : (((uint32_t)reinterpret_cast<uintptr_t>(p) & 15u) + rb + 15) / 16 * 16;
       };
       auto bring = [&](int arr, int r, const T* p) {
         bulk_load(smem + (size_t)st * stage_bytes + (size_t)(arr * R + r) * slot,
@@ -984,7 +990,7 @@ LnWs ln_bwd_ws(int T_, int d, int es, int v, bool add) {
   p.ct = ((d + p.E - 1) / p.E + 31) / 32 * 32;
   // stages of a row or two per row-sum warp where three of them fit
   const int sw = ln_sum_warps(p.cw, v, es);
-  const size_t rb = v == 1 ? ((size_t)d * es + 15) / 16 * 16 + 16 : (size_t)d * es;
+  const size_t rb = v * es < 16 ? ((size_t)d * es + 15) / 16 * 16 + 16 : (size_t)d * es;
   const size_t row = rb * (add ? 3 : 2), room = (p.cw == 8 ? 108 : 216) * 1024;
   p.grid = LN_SMS * (p.cw == 8 ? 2 : 1);
   int r = std::min(2 * sw, 8);
@@ -1017,7 +1023,7 @@ int ln_bwd_ws_go(const LnWs& p, const T* dy, int64_t lddy, const T* x, int64_t l
     LN_GO(8, 8);
   } else {
     if (p.E <= 2) {
-      if constexpr (V == 1) LN_GO(2, 8);
+      if constexpr (V <= 2) LN_GO(2, 8);
     } else if (p.E <= 4) {
       LN_GO(4, 8);
     } else {
@@ -1033,12 +1039,10 @@ template <class T, class W, int V>
 int ln_bwd_v(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* w, const float* mean,
              const float* rstd, const T* add, int64_t ldadd, int T_, int d, T* dx, float* part,
              int* nparts, cudaStream_t s) {
-  if constexpr (V * sizeof(T) == 16 || V == 1) {
-    const LnWs p = ln_bwd_ws(T_, d, sizeof(T), V, add != nullptr);
-    if (p.R && d > LN_NARROW) {
-      *nparts = p.grid;
-      return ln_bwd_ws_go<T, W, V>(p, dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T_, d, dx, part, s);
-    }
+  const LnWs p = ln_bwd_ws(T_, d, sizeof(T), V, add != nullptr);
+  if (p.R && d > LN_NARROW) {
+    *nparts = p.grid;
+    return ln_bwd_ws_go<T, W, V>(p, dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T_, d, dx, part, s);
   }
   // threads of a row: whole warps, or a power of two below
   int G = ((d + 7) / 8 + 31) / 32 * 32;
@@ -1089,7 +1093,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
   return ln_bwd_v<T, W, V>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, T_, d, dxt, part, nparts, s)
   if constexpr (sizeof(T) == 2) {
     if (v == 8) LN_V(8);
-    if (v == 2 && (d <= LN_NARROW || ln_bwd_ws(T_, d, 2, 1, add != nullptr).R == 0)) LN_V(2);
+    if (v == 2) LN_V(2);
   } else {
     if (v == 4) LN_V(4);
   }

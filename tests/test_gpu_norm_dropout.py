@@ -125,7 +125,8 @@ def test_layernorm_row_strides_and_alignment(dtype, d, pad, skip):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T,d,pad,skip", [(9600, 128, 3, 1), (9601, 128, 8, 8), (5001, 16, 8, 0), (5001, 33, 5, 2),
-                                          (4003, 200, 8, 4), (3000, 1000, 8, 4), (3000, 1001, 8, 3), (3000, 1001, 5, 0)])
+                                          (4003, 200, 8, 4), (3000, 1000, 8, 4), (3000, 1001, 8, 3), (3000, 1001, 5, 0),
+                                          (2500, 1029, 8, 3), (2500, 2053, 8, 7)])
 def test_layernorm_many_rows_inside_a_wider_matrix(T, d, pad, skip, dtype):
     """Each array at an offset of its own, NaN all around the rows."""
     gen = torch.Generator().manual_seed(T + d + pad + skip)
@@ -146,6 +147,20 @@ def test_layernorm_many_rows_inside_a_wider_matrix(T, d, pad, skip, dtype):
         ref = O.layernorm_fwd(f64(x), None, None, 1e-5)[0]
         within(y, ref, 256 * U * (np.abs(ref) + 2) + half_step(dtype) * np.abs(ref), "y")
         assert (buf[:off] == 7).all() and (buf[off + T * d:] == 7).all()
+
+
+@pytest.mark.parametrize("T,d", [(3000, 1002), (4000, 510), (2500, 2046), (1300, 3002), (1300, 7014)])
+def test_layernorm_many_rows_at_even_offsets(T, d):
+    """bf16 rows at 4-byte units, each array at another one, NaN all around the rows."""
+    gen = torch.Generator().manual_seed(T + d)
+
+    def cut(k):
+        big = torch.full((T + 2, d + 10), float("nan"), dtype=BF16, device="cuda")
+        view = big[1:T + 1, k:k + d]
+        view.copy_(draw(gen, T, d, dtype=BF16))
+        return view
+
+    check_ln(cut(2), draw(gen, d), draw(gen, d), dy=cut(4), add=cut(6))
 
 
 def test_layernorm_offset_does_not_cancel():
