@@ -983,9 +983,10 @@ LnWs ln_bwd_ws(int T_, int d, int es, int v, bool add) {
   LnWs p;
   if (d > LN_COLS) return p;
   // 8 column warps and two blocks per SM for up to 8 columns per thread, 16
-  // warps and one block beyond; as few columns per thread as there are threads
+  // warps and one block beyond; fp32 as few columns per thread as there are
+  // threads, bf16 at least 4 (100000 x 511: 143 us, with 2 155)
   p.cw = (d + 255) / 256 <= 8 ? 8 : 16;
-  p.E = std::max(v == 1 ? 2 : v, es == 4 && v > 1 ? 4 : 2);
+  p.E = es == 2 ? std::max(v, 4) : (v == 1 ? 2 : 4);
   while ((d + p.E - 1) / p.E > 32 * p.cw) p.E *= 2;
   p.ct = ((d + p.E - 1) / p.E + 31) / 32 * 32;
   // stages of a row or two per row-sum warp where three of them fit
@@ -1023,7 +1024,7 @@ int ln_bwd_ws_go(const LnWs& p, const T* dy, int64_t lddy, const T* x, int64_t l
     LN_GO(8, 8);
   } else {
     if (p.E <= 2) {
-      if constexpr (V <= 2) LN_GO(2, 8);
+      if constexpr (V == 1 && sizeof(T) == 4) LN_GO(2, 8);
     } else if (p.E <= 4) {
       LN_GO(4, 8);
     } else {
