@@ -163,6 +163,20 @@ def test_layernorm_many_rows_at_even_offsets(T, d):
     check_ln(cut(2), draw(gen, d), draw(gen, d), dy=cut(4), add=cut(6))
 
 
+@pytest.mark.parametrize("d", [63, 64, 512, 511, 1031])
+def test_layernorm_offsets_past_32_bits(d):
+    """Rows 2^20 elements apart, 2400 of them: element offsets past 2^31."""
+    T, ld = 2400, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    gen = torch.Generator().manual_seed(d)
+    big = torch.empty(T, ld, dtype=BF16, device="cuda")
+    x, dy, add = big[:, 16:16 + d], big[:, 4096:4096 + d], big[:, 8192:8192 + d]
+    for t in (x, dy, add):
+        t.copy_(draw(gen, T, d, dtype=BF16))
+    check_ln(x, draw(gen, d), draw(gen, d), dy=dy, add=add)
+
+
 def test_layernorm_offset_does_not_cancel():
     """A mean a thousand times the deviation: the variance comes from centred values."""
     gen = torch.Generator().manual_seed(3)

@@ -112,6 +112,31 @@ def test_exact_many_rows(T, d, f):
     assert torch.equal(y, (A @ w2).to(BF)) and torch.equal(dx, (d1 @ w1.T + d3 @ w3.T).to(BF))
 
 
+def test_exact_offsets_past_32_bits():
+    """H and dH of more than 2^31 elements."""
+    T, d, f = 600000, 8, 2048
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    c = exact_case(T, d, f, 1)
+    y, H = B.moe_shared_ffn_fwd(c["x"], c["w1"], c["w3"], c["w2"], addend=c["add"])
+    g = B.moe_shared_ffn_bwd(c["dout"], c["x"], c["w1"], c["w3"], c["w2"], H, addend=c["add"])
+    B.moe_check_status()
+    w1, w3, w2 = (c[n].double() for n in ("w1", "w3", "w2"))
+    dw = dict.fromkeys(("dw1", "dw3", "dw2"), 0.0)
+    for i in range(0, T, 50000):                  # as in test_exact_many_rows, rows by rows
+        r = slice(i, i + 50000)
+        x, do, add = (c[n][r].double() for n in ("x", "dout", "add"))
+        h1, h3 = x @ w1, x @ w3
+        da = do @ w2.T
+        d1, d3, A = da * h3, da * 32, 32 * h3
+        assert torch.equal(H[r].double(), torch.cat([h1, h3], 1)), i
+        assert torch.equal(y[r], (A @ w2 + add).to(BF)), i
+        assert torch.equal(g["dx"][r], (d1 @ w1.T + d3 @ w3.T + add).to(BF)), i
+        dw = dict(dw1=dw["dw1"] + x.T @ d1, dw3=dw["dw3"] + x.T @ d3, dw2=dw["dw2"] + A.T @ do)
+    for n, ref in dw.items():
+        assert torch.equal(g[n], ref.to(BF)), n
+
+
 def random_case(T, d, f, seed, scale=1.0):
     g = torch.Generator().manual_seed(seed)
     n = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(BF).cuda()  # noqa: E731
