@@ -858,7 +858,7 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
   int wpr = 1;
   while (wpr < 32 && npack > wpr * 32 * PT) wpr *= 2;
   while (wpr < 32 && npack > wpr * 32 && (int64_t)T_ * wpr < LN_SMS * 16) wpr *= 2;
-  const int nv = (npack + wpr * 32 - 1) / (wpr * 32);
+  const int nv = (int)(((int64_t)npack + wpr * 32 - 1) / (wpr * 32));   // npack may be 2^31 - 1
   const float inv_d = 1.0f / (float)d;
   ProfScope _ps("layernorm_fwd", s);
   {
@@ -920,7 +920,7 @@ int ln_fwd_units(const __nv_bfloat16* x, int64_t ldx, const W* w, const W* b, in
   if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15u) ||
       (ldx - d) % V)
     return 1;
-  const int units = (d + 2 * V - 2) / V;         // at most, over the offsets
+  const int units = (int)(((int64_t)d + 2 * V - 2) / V);   // at most, over the offsets
   int gw = 1;
   while (gw < 8 && units > gw * 32 * MAXNV) gw *= 2;
   if (units > gw * 32 * MAXNV || (int64_t)T_ * gw < LN_SMS * 8) return 1;
@@ -1080,7 +1080,7 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
     *nparts = LN_SLICES;
     if (part) {
       ProfScope _ps("layernorm_bwd_cols", s);
-      const dim3 grid((d + 255) / 256, LN_SLICES);
+      const dim3 grid((unsigned)(((int64_t)d + 255) / 256), LN_SLICES);
       k_ln_bwd_cols<T><<<grid, 256, 0, s>>>(dyt, lddy, xt, ldx, mean, rstd, part, T_, d);
       MOE_CHECK_LAUNCH("layernorm_bwd_cols");
     }
