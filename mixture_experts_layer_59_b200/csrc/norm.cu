@@ -358,9 +358,36 @@ k_ln_fwd_units(const __nv_bfloat16* x, int64_t ldx, const W* __restrict__ w, con
   }
 }
 
+// A thread's sums over a row or column too long for registers: f adds element i
+// to the N sums, for i = first, first + step, .. below end.  LONG: more than
+// LONG_SUM elements, of which that many at a time add up in fp32 and those sums
+// in fp64, so that the roundings stay as few as elsewhere (a constant row of
+// 2^28 columns added up in fp32 alone: its mean 0.25 % off).
+constexpr int LONG_SUM = 64;
+template <bool LONG, int N, class F>
+__device__ __forceinline__ void strided_sums(int64_t first, int64_t step, int64_t end,
+                                             float (&sums)[N], F f) {
+  int64_t i = first;
+  double total[N] = {};
+  if (LONG)
+    while (i + (LONG_SUM - 1) * step < end) {
+      float s[N] = {};
+#pragma unroll 4
+      for (int k = 0; k < LONG_SUM; ++k, i += step) f(i, s);
+#pragma unroll
+      for (int n = 0; n < N; ++n) total[n] += s[n];
+    }
+#pragma unroll
+  for (int n = 0; n < N; ++n) sums[n] = 0.f;
+  for (; i < end; i += step) f(i, sums);
+  if (LONG)
+#pragma unroll
+    for (int n = 0; n < N; ++n) sums[n] = (float)(total[n] + sums[n]);
+}
+
 // Rows wider than the registers of a block: three passes over the row, the
 // second and third from the caches.
-template <class T, class W>
+template <class T, class W, bool LONG>
 __global__ void __launch_bounds__(1024)
 k_ln_fwd_wide(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, T* y,
               float* __restrict__ mean, float* __restrict__ rstd, int d, float eps) {
@@ -368,16 +395,15 @@ k_ln_fwd_wide(const T* x, int64_t ldx, const W* __restrict__ w, const W* __restr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;
   const T* xr = x + row * ldx;
-  float s = 0.f;
-  for (int64_t c = threadIdx.x; c < d; c += blockDim.x) s += to_f(xr[c]);
+  float s[1];
+  strided_sums<LONG>(threadIdx.x, blockDim.x, d, s, [&](int64_t c, float* a) { a[0] += to_f(xr[c]); });
   const float inv_d = 1.0f / (float)d;
-  const float mu = group_sum(s, red[0], 32, warp, lane) * inv_d;
-  s = 0.f;
-  for (int64_t c = threadIdx.x; c < d; c += blockDim.x) {
+  const float mu = group_sum(s[0], red[0], 32, warp, lane) * inv_d;
+  strided_sums<LONG>(threadIdx.x, blockDim.x, d, s, [&](int64_t c, float* a) {
     const float e = to_f(xr[c]) - mu;
-    s = fmaf(e, e, s);
-  }
-  const float rs = rsqrtf(group_sum(s, red[1], 32, warp, lane) * inv_d + eps);
+    a[0] = fmaf(e, e, a[0]);
+  });
+  const float rs = rsqrtf(group_sum(s[0], red[1], 32, warp, lane) * inv_d + eps);
   for (int64_t c = threadIdx.x; c < d; c += blockDim.x) {
     float e = (to_f(xr[c]) - mu) * rs;
     if (w) e *= to_f(w[c]);
@@ -782,23 +808,23 @@ k_ln_reduce(const float* __restrict__ part, int nparts, int d, float* __restrict
 
 // Rows wider than a block's registers: the column sums first (a strip of 256
 // columns over a slice of the rows per block), then dx row by row.
-template <class T>
+template <class T, bool LONG>
 __global__ void __launch_bounds__(256)
 k_ln_bwd_cols(const T* dy, int64_t lddy, const T* x, int64_t ldx, const float* __restrict__ mean,
               const float* __restrict__ rstd, float* __restrict__ part, int T_, int d) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= d) return;
-  float aw = 0.f, ab = 0.f;
-  for (int64_t t = blockIdx.y; t < T_; t += gridDim.y) {
+  float s[2];
+  strided_sums<LONG>(blockIdx.y, gridDim.y, T_, s, [&](int64_t t, float* a) {
     const float dyv = to_f(dy[t * lddy + c]);
-    aw = fmaf(dyv, (to_f(x[t * ldx + c]) - mean[t]) * rstd[t], aw);
-    ab += dyv;
-  }
-  part[(size_t)blockIdx.y * 2 * d + c] = aw;
-  part[(size_t)blockIdx.y * 2 * d + d + c] = ab;
+    a[0] = fmaf(dyv, (to_f(x[t * ldx + c]) - mean[t]) * rstd[t], a[0]);
+    a[1] += dyv;
+  });
+  part[(size_t)blockIdx.y * 2 * d + c] = s[0];
+  part[(size_t)blockIdx.y * 2 * d + d + c] = s[1];
 }
 
-template <class T, class W>
+template <class T, class W, bool LONG>
 __global__ void __launch_bounds__(1024)
 k_ln_bwd_wide(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
               const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
@@ -807,15 +833,15 @@ k_ln_bwd_wide(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __res
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;
   const float mu = mean[row], rs = rstd[row];
-  float s1 = 0.f, s2 = 0.f;
-  for (int64_t c = threadIdx.x; c < d; c += blockDim.x) {
+  float s[2];
+  strided_sums<LONG>(threadIdx.x, blockDim.x, d, s, [&](int64_t c, float* a) {
     const float g = to_f(dy[row * lddy + c]) * (w ? to_f(w[c]) : 1.f);
-    s1 += g;
-    s2 = fmaf(g, (to_f(x[row * ldx + c]) - mu) * rs, s2);
-  }
+    a[0] += g;
+    a[1] = fmaf(g, (to_f(x[row * ldx + c]) - mu) * rs, a[1]);
+  });
   const float inv_d = 1.0f / (float)d;
-  s1 = group_sum(s1, red[0], 32, warp, lane) * inv_d;
-  s2 = group_sum(s2, red[1], 32, warp, lane) * inv_d;
+  const float s1 = group_sum(s[0], red[0], 32, warp, lane) * inv_d;
+  const float s2 = group_sum(s[1], red[1], 32, warp, lane) * inv_d;
   for (int64_t c = threadIdx.x; c < d; c += blockDim.x) {
     const float g = to_f(dy[row * lddy + c]) * (w ? to_f(w[c]) : 1.f);
     float v = rs * (g - s1 - (to_f(x[row * ldx + c]) - mu) * rs * s2);
@@ -893,8 +919,10 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
     else if (wpr == 16) LN_GO(NV, 16);                                                        \
     else LN_GO(NV, 32);                                                                       \
   } while (0)
-  if (nv > PT) k_ln_fwd_wide<T, W><<<T_, 1024, 0, s>>>(x, ldx, w, b, y, mean, rstd, d, eps);
-  else if (nv <= 2) LN_W(2);
+  if (nv > PT) {
+    auto* kernel = d <= LONG_SUM * 1024 ? k_ln_fwd_wide<T, W, false> : k_ln_fwd_wide<T, W, true>;
+    kernel<<<T_, 1024, 0, s>>>(x, ldx, w, b, y, mean, rstd, d, eps);
+  } else if (nv <= 2) LN_W(2);
   else if (nv <= 4) LN_W(4);
   else if constexpr (PT == 8 && V * sizeof(T) == 16) LN_W(8);
   else if constexpr (PT > 4) {
@@ -1081,11 +1109,13 @@ int ln_bwd_t(const void* dy, int64_t lddy, const void* x, int64_t ldx, const voi
     if (part) {
       ProfScope _ps("layernorm_bwd_cols", s);
       const dim3 grid((unsigned)(((int64_t)d + 255) / 256), LN_SLICES);
-      k_ln_bwd_cols<T><<<grid, 256, 0, s>>>(dyt, lddy, xt, ldx, mean, rstd, part, T_, d);
+      auto* kernel = T_ <= LONG_SUM * LN_SLICES ? k_ln_bwd_cols<T, false> : k_ln_bwd_cols<T, true>;
+      kernel<<<grid, 256, 0, s>>>(dyt, lddy, xt, ldx, mean, rstd, part, T_, d);
       MOE_CHECK_LAUNCH("layernorm_bwd_cols");
     }
     ProfScope _ps("layernorm_bwd", s);
-    k_ln_bwd_wide<T, W><<<T_, 1024, 0, s>>>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, dxt, d);
+    auto* kernel = d <= LONG_SUM * 1024 ? k_ln_bwd_wide<T, W, false> : k_ln_bwd_wide<T, W, true>;
+    kernel<<<T_, 1024, 0, s>>>(dyt, lddy, xt, ldx, wt, mean, rstd, at, ldadd, dxt, d);
     MOE_CHECK_LAUNCH("layernorm_bwd");
     return MOE_OK;
   }
