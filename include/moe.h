@@ -568,6 +568,18 @@ int moe_check_status(void* stream);
 int moe_debug_expire_next_wait(long long wait_ns);
 
 /*
+ * moe_debug_shared_ffn_plan -- test hook (host only, no device needed): how
+ * the shared FFN would cut one of its products, product 0: H = x [W1 | W3],
+ * 1: y = A W2, 2: dA = dout W2^T, 3: dx = dH [W1 | W3]^T, 4: the weights'
+ * gradients.  plan[7] out: tile columns of a split tile (128 or 256), 0: CTA
+ * pairs with tiles of 256 x 256; CTAs that share a tile (split) or 2; tiles;
+ * and for pairs how many of them are computed whole, the k-blocks of a share
+ * of the others (0: none), the k-blocks a shared tile counts for; k-blocks of
+ * a tile.  MOE_OK, or the code with which the call itself refuses the sizes.
+ */
+int moe_debug_shared_ffn_plan(int T, int d, int f, int product, int* plan);
+
+/*
  * Measurement hook (the pages have no counterpart; it serves the benchmark).
  * moe_profile_enable(1): from now on every kernel the library launches is
  * bracketed by two CUDA events recorded on the kernel's own stream.

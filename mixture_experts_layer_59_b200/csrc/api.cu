@@ -1035,6 +1035,15 @@ int moe_shared_ffn_bwd(const void* dout, const void* x, const void* w1, const vo
                  w.scratch, s);
 }
 
+int moe_debug_shared_ffn_plan(int T, int d, int f, int product, int* plan) {
+  if (int rc = check_ffn(T, d, f, MOE_BF16)) return rc;
+  if (T == 0 || product < 0 || product > 4)
+    return fail(MOE_ERR_INVALID_ARG, "T must be > 0, product 0 .. 4");
+  REQUIRE_PTR(plan);
+  ffn_debug_plan(T, d, f, product, plan);
+  return MOE_OK;
+}
+
 int moe_check_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");

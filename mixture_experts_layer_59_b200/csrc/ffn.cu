@@ -976,10 +976,15 @@ int count_tiles(int kind, int d, int f, int T, int rows, int cols) {
 // Rows of A's boxes: what exists, in the 8-row units of the swizzle.
 int a_box_rows(int T) { return T >= BM ? BM : (T + 7) / 8 * 8; }
 
+// k-blocks of a tile of one product.
+int count_kbs(int kind, int T, int d, int f) {
+  const int kd = (d + BK - 1) / BK, kf = (f + BK - 1) / BK, kt = (T + BK - 1) / BK;
+  return kind == F_DW ? kt : (kind == F_DX ? 2 * kf : (kind == F_DOWN ? kf : kd));
+}
+
 FPlan f_plan(int kind, int T, int d, int f) {
   FPlan p = {};
-  const int kd = (d + BK - 1) / BK, kf = (f + BK - 1) / BK, kt = (T + BK - 1) / BK;
-  const int kbs = kind == F_DW ? kt : (kind == F_DX ? 2 * kf : (kind == F_DOWN ? kf : kd));
+  const int kbs = count_kbs(kind, T, d, f);
   // Clocks, for comparison only.  A pair's k-block takes 700 (measured at
   // 8192 x 7168 x 2048; 512 of MMAs), a split CTA's what 64 bytes per clock
   // bring in.  Whole waves of pairs; the rest shared where that ends the wave
@@ -993,7 +998,7 @@ FPlan f_plan(int kind, int T, int d, int f) {
   p.whole = p.tiles;
   int64_t best = (int64_t)(waves + (rem > 0)) * kbs * 700;
   auto share = [&](int k, int span, int parts) {
-    const int64_t t = (int64_t)waves * kbs * 700 + k * 700 + 3000 + parts * 2000;
+    const int64_t t = ((int64_t)waves * kbs + k) * 700 + 3000 + parts * 2000;
     if (t < best) {
       best = t;
       p.whole = p.tiles - rem;
@@ -1164,6 +1169,13 @@ struct FCall {
 size_t ffn_scratch_bytes(int T, int d, int f, bool bwd) {
   const FScratch z = ffn_scratch(T, d, f, bwd);
   return z.part_bytes + align_up(z.counts * sizeof(int), 256);
+}
+
+void ffn_debug_plan(int T, int d, int f, int product, int* out) {
+  const FPlan p = f_plan(product, T, d, f);
+  const int v[] = {p.split ? p.bn : 0, p.split ? p.cluster : 2, p.tiles, p.whole, p.share, p.span,
+                   count_kbs(product, T, d, f)};
+  std::copy(std::begin(v), std::end(v), out);
 }
 
 int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, void* scratch,

@@ -136,6 +136,8 @@ struct FfnDense {
 size_t ffn_scratch_bytes(int T, int d, int f, bool bwd);
 int ffn_fwd(const FfnDense& p, const void* addend, void* H, void* act, void* y, void* scratch,
             cudaStream_t s);
+// The plan of one product (0 .. 4: UP, DOWN, DAP, DX, DW) as 7 numbers.
+void ffn_debug_plan(int T, int d, int f, int product, int* out);
 // dH [T, 2f] and act [T, f]: workspace.
 int ffn_bwd(const FfnDense& p, const void* dout, const void* H, const void* addend, void* dH,
             void* act, void* dx, void* dw1, void* dw3, void* dw2, void* scratch, cudaStream_t s);

@@ -1,0 +1,27 @@
+"""How the shared FFN cuts its products, asked of the library (no GPU needed)."""
+import ctypes
+from collections import namedtuple
+
+from mixture_experts_layer_59_b200 import binding as B
+
+PRODUCTS = ("UP", "DOWN", "DAP", "DX", "DW")
+PAIRS = 74
+Plan = namedtuple("Plan", "bn cluster tiles whole share span kbs")
+
+
+def plan(T, d, f, product):
+    out = (ctypes.c_int * 7)()
+    rc = B.lib().moe_debug_shared_ffn_plan(T, d, f, product, out)
+    assert rc == 0, (T, d, f, rc)
+    return Plan(*out)
+
+
+def kind(p):
+    """split tiles of 128 or 256 columns, one CTA each or several; pairs: whole
+    tiles only, or the last ones shared, cut alike or anywhere."""
+    if p.bn:
+        return f"split {p.bn}" + (" cluster" if p.cluster > 1 else "")
+    return "whole" if p.share == 0 else ("shared alike" if p.span % p.share == 0 else "shared anywhere")
+
+
+KINDS = ("split 128", "split 128 cluster", "split 256", "split 256 cluster", "whole", "shared alike", "shared anywhere")
