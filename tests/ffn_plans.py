@@ -25,3 +25,13 @@ def kind(p):
 
 
 KINDS = ("split 128", "split 128 cluster", "split 256", "split 256 cluster", "whole", "shared alike", "shared anywhere")
+
+# Sizes of the GPU tests: between them every kind of cut for every product, with
+# widths and row counts that tiles and boxes do not divide.
+EXACT_SIZES = [(1, 72, 72), (200, 4096, 2048), (259, 6864, 72), (300, 4096, 2048), (700, 7168, 2048), (1493, 4104, 2056),
+               (1500, 4096, 2048), (2500, 1024, 2048), (2511, 1032, 2056), (2971, 136, 3272), (4630, 176, 1016),
+               (6207, 544, 272)]
+# The same for outputs and workspaces with guard bands: pairs with shared tiles and
+# clipped edges, clusters.
+GUARD_SIZES = [(300, 1000, 680), (259, 6864, 72), (1493, 4104, 2056), (2511, 1032, 2056), (2971, 136, 3272),
+               (4321, 1992, 1352), (5000, 2048, 520), (10000, 2048, 648)]

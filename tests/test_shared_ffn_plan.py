@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-from ffn_plans import KINDS, PAIRS, PRODUCTS, kind, plan
+from ffn_plans import EXACT_SIZES, GUARD_SIZES, KINDS, PAIRS, PRODUCTS, kind, plan
 from mixture_experts_layer_59_b200 import binding as B
 
 
@@ -76,3 +76,13 @@ def test_every_k_block_is_in_one_share():
             check_shares(p)
     # the planner does choose each of them for each product
     assert set(seen) == {(a, b) for a in PRODUCTS for b in KINDS}
+
+
+def test_gpu_tests_cover_every_cut():
+    everything = {(a, b) for a in PRODUCTS for b in KINDS}
+    covered = {(a, kind(plan(*s, i))) for s in EXACT_SIZES for i, a in enumerate(PRODUCTS)}
+    assert covered == everything, everything - covered
+    guarded = {(a, kind(plan(*s, i))) for s in GUARD_SIZES for i, a in enumerate(PRODUCTS)}
+    pairs = {(a, b) for a in PRODUCTS for b in KINDS if b.startswith("shared")}
+    assert len(guarded & pairs) >= 8 and {a for a, _ in guarded & pairs} >= {"UP", "DOWN", "DAP", "DX"}, guarded
+    assert {a for a, b in guarded if b == "split 128 cluster"} >= {"UP", "DAP", "DX"}, guarded
