@@ -476,6 +476,8 @@ int moe_balance_loss(const int32_t* idx, const float* gate, int T, int E, int k,
  *   T = 0.  Sums run in a fixed order (deterministic).  ws: at least
  *   moe_layernorm_bwd_workspace_size() bytes, 16-byte aligned (not needed
  *   without dweight and dbias).
+ *   Over many rows its waits are bounded as the GEMMs' are: if one expires,
+ *   dx, dweight and dbias are undefined and moe_check_status() tells.
  *   Both calls may read a row in the 16-byte units that hold it; the other
  *   bytes of its first and last unit do not reach the results.
  */
@@ -557,15 +559,18 @@ int moe_check_status(void* stream);
 
 /*
  * moe_debug_expire_next_wait -- test hook for the bounded device waits (the
- * pages have no counterpart).  The next tensor-core GEMM launch of the
- * library (on any stream of this process) runs with its TMA producer issuing
- * no copies and every bounded wait limited to wait_ns nanoseconds, so that
- * the MMA issuer's wait for a full stage expires with nothing in flight; the
- * hook then resets itself.  That launch's outputs are undefined and
+ * pages have no counterpart).  The next launch of the library (on any stream
+ * of this process) of a tensor-core GEMM or of the layer norm's backward pass
+ * over many rows runs with its producer issuing no copies and every bounded
+ * wait limited to wait_ns nanoseconds, so that the wait for a full stage
+ * expires with nothing in flight; the hook then resets itself.  That launch's outputs are undefined and
  * moe_check_status() afterwards returns MOE_ERR_DEVICE_TIMEOUT.  wait_ns <= 0
  * cancels a pending request.  Returns MOE_OK.
+ * moe_debug_expire_later_wait -- the same after `skip` such launches have
+ * passed as usual (a later product of one call).
  */
 int moe_debug_expire_next_wait(long long wait_ns);
+int moe_debug_expire_later_wait(int skip, long long wait_ns);
 
 /*
  * moe_debug_shared_ffn_plan -- test hook (host only, no device needed): how

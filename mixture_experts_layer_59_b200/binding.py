@@ -39,7 +39,7 @@ EXPORTS = [
     "moe_token_bwd", "moe_layernorm_fwd", "moe_layernorm_bwd_workspace_size", "moe_layernorm_bwd",
     "moe_dropout_fwd", "moe_dropout_bwd", "moe_shared_ffn_fwd_workspace_size",
     "moe_shared_ffn_fwd", "moe_shared_ffn_bwd_workspace_size", "moe_shared_ffn_bwd",
-    "moe_debug_shared_ffn_plan",
+    "moe_debug_shared_ffn_plan", "moe_debug_expire_later_wait",
 ]
 
 _lib = None
@@ -102,6 +102,7 @@ _SIGS = {
     "moe_shared_ffn_bwd_workspace_size": (_sz, [_i] * 4),
     "moe_shared_ffn_bwd": (_i, [_vp] * 7 + [_i] * 4 + [_vp] * 5 + [_sz, _vp]),
     "moe_debug_shared_ffn_plan": (_i, [_i] * 4 + [_vp]),
+    "moe_debug_expire_later_wait": (_i, [_i, ctypes.c_longlong]),
 }
 
 

@@ -48,9 +48,11 @@ int* status_ptr() {
 }
 
 static std::atomic<long long> g_debug_expire{0};
+static std::atomic<int> g_debug_skip{0};   // launches that pass first
 
 long long take_debug_expire() {
   if (g_debug_expire.load(std::memory_order_relaxed) == 0) return 0;
+  if (g_debug_skip.load() > 0 && g_debug_skip.fetch_sub(1) > 0) return 0;
   return g_debug_expire.exchange(0);
 }
 
@@ -1066,6 +1068,11 @@ int moe_check_status(void* stream) {
 }
 
 int moe_debug_expire_next_wait(long long wait_ns) {
+  return moe_debug_expire_later_wait(0, wait_ns);
+}
+
+int moe_debug_expire_later_wait(int skip, long long wait_ns) {
+  g_debug_skip.store(skip > 0 ? skip : 0);
   g_debug_expire.store(wait_ns > 0 ? wait_ns : 0);
   return MOE_OK;
 }

@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(ln_ws_threads(CW, V, sizeof(T)), CW == 8 ? 2 :
 k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restrict__ w,
             const float* __restrict__ mean, const float* __restrict__ rstd, const T* add,
             int64_t ldadd, T* dx, float* __restrict__ part, int T_, int d, float inv_d, int R,
-            int stages, int ct, int* status) {
+            int stages, int ct, int* status, uint64_t wait_ns, int dbg_no_load) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[LN_STAGES], ready[LN_STAGES], empty[LN_STAGES];
   // per row of a stage, as pairs of the same value: -mean, rstd, -s1 / d, -s2 / d
@@ -619,7 +619,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
   };
   if (warp == CW + SW) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) {
+    if (lane == 0 && !dbg_no_load) {
       auto bytes_of = [&](const T* p) {
         return UNITS ? rb : (((uint32_t)reinterpret_cast<uintptr_t>(p) & 15u) + rb + 15) / 16 * 16;
       };
@@ -629,7 +629,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
                   bytes_of(p), &full[st]);
       };
       for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
-        if (!bounded_wait(&empty[st], phase ^ 1, &s_abort, status, 6, WAIT_LIMIT_NS)) break;
+        if (!bounded_wait(&empty[st], phase ^ 1, &s_abort, status, 6, wait_ns)) break;
         const int rows = rows_of(t);
         uint32_t bytes = 0;
         for (int r = 0; r < rows; ++r) {
@@ -655,7 +655,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
       const bool any = turn < rows;                // its statistics early
       const float mu0 = any ? mean[t * R + turn] : 0.f, rs0 = any ? rstd[t * R + turn] : 0.f;
       // a warp without a row waits too: it must not run ahead of the stage
-      bounded_wait(&full[st], phase, &s_abort, status, 7, WAIT_LIMIT_NS);
+      bounded_wait(&full[st], phase, &s_abort, status, 7, wait_ns);
       for (int r = turn; r < rows; r += SW) {
         const bool first = r == turn;
         const int64_t row = t * R + r;
@@ -709,7 +709,7 @@ k_ln_bwd_ws(const T* dy, int64_t lddy, const T* x, int64_t ldx, const W* __restr
     }
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, advance()) {
       const int rows = sg < nsg ? rows_of(t) : 0;   // threads past the last whole ct rest
-      bounded_wait(&ready[st], phase, &s_abort, status, 8, WAIT_LIMIT_NS);
+      bounded_wait(&ready[st], phase, &s_abort, status, 8, wait_ns);
 #pragma unroll 2
       for (int r = sg; r < rows; r += nsg) {
         const int64_t row = t * R + r;
@@ -1037,13 +1037,14 @@ int ln_bwd_ws_go(const LnWs& p, const T* dy, int64_t lddy, const T* x, int64_t l
                  const float* mean, const float* rstd, const T* add, int64_t ldadd, int T_, int d,
                  T* dx, float* part, cudaStream_t s) {
   ProfScope _ps("layernorm_bwd", s);
+  const long long dbg = take_debug_expire();
 #define LN_GO(E, CW)                                                                           \
   do {                                                                                         \
     if (cudaError_t e = smem_limit<k_ln_bwd_ws<T, W, V, E, CW>>((CW == 8 ? 108 : 216) * 1024)) \
       return cuda_fail(e, "layernorm smem attribute");                                         \
     k_ln_bwd_ws<T, W, V, E, CW><<<p.grid, ln_ws_threads(CW, V, sizeof(T)), p.bytes, s>>>(                  \
         dy, lddy, x, ldx, w, mean, rstd, add, ldadd, dx, part, T_, d, 1.0f / (float)d, p.R,    \
-        p.stages, p.ct, status_ptr());                                                         \
+        p.stages, p.ct, status_ptr(), dbg > 0 ? (uint64_t)dbg : WAIT_LIMIT_NS, dbg > 0);       \
   } while (0)
   if (p.cw == 16) {
     if (p.E <= 8) LN_GO(8, 16);
