@@ -887,22 +887,20 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
   const int nv = (int)(((int64_t)npack + wpr * 32 - 1) / (wpr * 32));   // npack may be 2^31 - 1
   const float inv_d = 1.0f / (float)d;
   ProfScope _ps("layernorm_fwd", s);
-  {
-    // A row in a warp or a part of it, 256 threads to a block: two packs of
-    // 16 bytes (four of 4) per lane, or 8 single elements (200000 x 127 bf16: 37 us, 94 by units).
-    constexpr int PL = V == 1 ? 8 : (V * sizeof(T) == 16 ? 2 : 4);
-    if (npack <= 32 * PL && T_ > LN_SMS * 16) {
+  // Many rows, each in a warp or a part of it, 256 threads to a block: two packs of
+  // 16 bytes (four of 4) per lane, or 8 single elements (200000 x 127 bf16: 37 us, 94 by units).
+  constexpr int PL = V == 1 ? 8 : (V * sizeof(T) == 16 ? 2 : 4);
+  if (npack <= 32 * PL && T_ >= LN_SMS * 16) {
 #define LN_GO(LPR)                                                                             \
   k_ln_fwd<T, W, V, PL, 1, LPR><<<(T_ + (int64_t)(256 / LPR) - 1) / (256 / LPR), 256, 0, s>>>( \
       x, ldx, w, b, y, mean, rstd, T_, d, inv_d, eps)
-      if (npack <= 4 * PL) LN_GO(4);
-      else if (npack <= 8 * PL) LN_GO(8);
-      else if (npack <= 16 * PL) LN_GO(16);
-      else LN_GO(32);
+    if (npack <= 4 * PL) LN_GO(4);
+    else if (npack <= 8 * PL) LN_GO(8);
+    else if (npack <= 16 * PL) LN_GO(16);
+    else LN_GO(32);
 #undef LN_GO
-      MOE_CHECK_LAUNCH("layernorm_fwd");
-      return MOE_OK;
-    }
+    MOE_CHECK_LAUNCH("layernorm_fwd");
+    return MOE_OK;
   }
 #define LN_GO(NV, WPR)                                                                        \
   do {                                                                                        \
@@ -912,8 +910,10 @@ int ln_fwd_v(const T* x, int64_t ldx, const W* w, const W* b, int T_, int d, flo
   } while (0)
 #define LN_W(NV)                                                                              \
   do {                                                                                        \
-    if (wpr == 1) LN_GO(NV, 1);                                                               \
-    else if (wpr == 2) LN_GO(NV, 2);                                                          \
+    if (wpr == 1) {                                                                           \
+      /* one pack per lane, or many rows of more than PL: rows between were launched above */ \
+      if constexpr (NV <= 2 || NV > PL) LN_GO(NV, 1);                                         \
+    } else if (wpr == 2) LN_GO(NV, 2);                                                        \
     else if (wpr == 4) LN_GO(NV, 4);                                                          \
     else if (wpr == 8) LN_GO(NV, 8);                                                          \
     else if (wpr == 16) LN_GO(NV, 16);                                                        \

@@ -8,6 +8,7 @@ import torch
 
 from mixture_experts_layer_59_b200 import binding as B
 from oracle import block_oracle as O
+from test_gpu_norm_dropout import check_ln
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -65,6 +66,17 @@ def test_layernorm_outputs_left_out(T, d):
         assert torch.equal(dx, want["dx"])
         assert torch.equal(gw, want["dweight"]) if dw else bool((gw == 3).all())
         assert torch.equal(gb, want["dbias"]) if db else bool((gb == 3).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [2367, 2368, 2369])
+def test_layernorm_where_the_launch_shape_changes(T, dtype):
+    """Row counts around 16 warps per SM, widths around each share of a warp
+    (tolerances: those of the norm's tests)."""
+    gen = torch.Generator().manual_seed(T)
+    for d in (30, 62, 64, 66, 126, 128, 254, 255, 256, 257, 258, 510, 512, 514, 1022, 1023, 1024, 1025):
+        x = (torch.randn(T, d, generator=gen) * 2 + 0.5).to(dtype).cuda()
+        check_ln(x, torch.randn(d, generator=gen).cuda(), torch.randn(d, generator=gen).cuda())
 
 
 def test_layernorm_of_most_rows():
