@@ -1167,7 +1167,8 @@ int launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ld
              ? ln_bwd_t<float, __nv_bfloat16>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, &nparts, s)
              : ln_bwd_t<float, float>(dy, lddy, x, ldx, w, mean, rstd, add, ldadd, T, d, dx, part, &nparts, s);
   if (rc || part == nullptr) return rc;
-  // launched as a dependent: its blocks are ready when the last row is done
+  // launched as a dependent: neither kernel above triggers it early, so its
+  // blocks start when the last of theirs has left, before the stream's full wait
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
