@@ -14,6 +14,13 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def give_memory_back():
+    """The large buffers of a test are not kept from those after it."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def need(gb):
     if torch.cuda.mem_get_info()[0] < gb << 30:
         pytest.skip(f"needs {gb} GB")

@@ -12,6 +12,13 @@ BF16, F32 = torch.bfloat16, torch.float32
 STEP = 1 << 27          # columns compared at a time
 
 
+@pytest.fixture(autouse=True)
+def give_memory_back():
+    """The large buffers of a test are not kept from those after it."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def need(gb):
     if torch.cuda.mem_get_info()[0] < gb << 30:
         pytest.skip(f"needs {gb} GB")
