@@ -9,6 +9,7 @@ import torch
 from mixture_experts_layer_59_b200 import binding as B
 from oracle import block_oracle as O
 from test_gpu_norm_dropout import check_ln
+from test_gpu_shared_ffn import random_case
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -147,3 +148,28 @@ def test_dropout_blocks_past_32_bits():
     for lo, hi in ((0, 1000), ((1 << 35) - 1000, (1 << 35) + 1000), (m - 3000, m)):
         keep = O.dropout_keep(123, 45, lo, hi - lo, 0.5)
         assert (y[lo:hi].double().cpu().numpy() == keep * 2.0).all(), lo
+
+
+def test_shared_ffns_and_norms_on_three_streams_at_once():
+    """Pairs with shared tiles, clusters and a norm's backward pass in flight together,
+    each with buffers of its own: the results they have alone."""
+    jobs = []
+    for T, d, f in ((1493, 4104, 2056), (300, 1000, 680), (700, 7168, 2048)):
+        c = random_case(T, d, f, T)
+        gen = torch.Generator().manual_seed(T)
+        x, dy, w = (torch.randn(*s, generator=gen).cuda() for s in ((4000, 1037), (4000, 1037), (1037,)))
+
+        def job(c=c, x=x, dy=dy, w=w, **at):
+            ws = (c["w1"], c["w3"], c["w2"])
+            y, H = B.moe_shared_ffn_fwd(c["x"], *ws, addend=c["add"], **at)
+            g = B.moe_shared_ffn_bwd(c["dout"], c["x"], *ws, H, addend=c["add"], **at)
+            n, mean, rstd = B.moe_layernorm_fwd(x, w, **at)
+            return [y, H, n, *g.values(), *B.moe_layernorm_bwd(dy, x, w, mean, rstd, **at).values()]
+        jobs.append((job, job(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [job(stream=s) for job, _, s in jobs]
+        torch.cuda.synchronize()
+        for (_, want, _), out in zip(jobs, got):
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+    B.moe_check_status()
