@@ -713,7 +713,8 @@ def moe_dropout_fwd(x, p, rng, residual=None, out=None, stream=None):
 
 
 def moe_dropout_bwd(dout, p, rng, dx=None, stream=None):
-    """Gradient of moe_dropout_fwd for its x (the residual's is dout itself)."""
+    """Gradient of moe_dropout_fwd for its x (the residual's is dout itself); rng as
+    it was at the forward call."""
     dt, dev = _code("dout", dout), dout.device
     _arg("dout", dout, dout.shape, dout.dtype, dev)
     _arg("rng", rng, (2,), torch.int64, dev)

@@ -169,7 +169,9 @@ class MoEBlockStep:
     def forward(self, x, ln, experts, shared, rng, stream=None, **route):
         """ln: (weight, bias); experts: (w_gate, w1, w3, w2); shared: (w1, w3,
         w2); rng: int64 [2] on the device, (seed, offset); route: what
-        MoELayerStep.forward takes besides."""
+        MoELayerStep.forward takes besides.  backward() reads x, the weights and
+        rng again (it draws the same mask anew): leave them as they are until
+        it has run."""
         self._saved = (x, ln, shared, rng)
         B.moe_layernorm_fwd(x, *ln, eps=self.eps, y=self.n, mean=self.mean, rstd=self.rstd,
                             stream=stream)
