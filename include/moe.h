@@ -326,7 +326,8 @@ int moe_combine(const void* Y_perm, const float* row_gate, const int32_t* slot_r
  *   (MOE_GATE_SOFTMAX_TOPK: dl_te += [e in K_t] p_e a_e - p_e sum_i g_i a_i).
  *   Outputs: dx [T,d] (dtype), dw_gate [d,E] fp32, dw1, dw3 [E,d,f] (dtype),
  *   dw2 [E,f,d] (dtype), dS [cap] fp32 (may be NULL), dlogits [T,E] fp32
- *   (may be NULL).  Every output element is written (no accumulation).
+ *   (may be NULL).  Every output element is written (no accumulation): dS is 0
+ *   in rows that hold no token.
  */
 size_t moe_layer_bwd_workspace_size(int T, int d, int f, int E, int k, int dtype);
 int moe_layer_bwd(const void* dout, const void* x, const void* w_gate,

@@ -484,13 +484,15 @@ static int token_bwd_impl(const void* dxp, const float* ds_part, int nparts, con
                           const float* gate_grad, const float* logits, int gate_mode,
                           const float* row_gate, const int32_t* slot_row,
                           const int32_t* extra_row, int T, int d, int E, int k, int dtype,
-                          int router_grad, void* dx, float* dw_gate, float* dS, float* dlogits,
-                          const TokenWs& w, cudaStream_t s) {
+                          int router_grad, void* dx, float* dw_gate, const int32_t* row_token,
+                          const int32_t* offsets, float* dS, float* dlogits, const TokenWs& w,
+                          cudaStream_t s) {
   int rc;
   float* dl = dlogits ? dlogits : w.dl;
   const bool tc_router = router_grad && w.dl_hi != nullptr;
   if ((rc = launch_router_bwd(ds_part, nparts, idx, gate, row_gate, slot_row, extra_row,
-                              gate_grad, logits, gate_mode, T, E, k, dl, dS,
+                              gate_grad, logits, gate_mode, T, E, k, dl, row_token, offsets,
+                              T * k + E * 128, dS,
                               tc_router ? w.dl_hi : nullptr,
                               tc_router ? w.dl_lo : nullptr, s)))
     return rc;
@@ -592,7 +594,7 @@ static int layer_bwd_impl(const void* dout, const void* x, const void* w_gate, c
   }
   return token_bwd_impl(w.dxp, w.ds, w.nparts, x, w_gate, idx, gate, gate_grad, logits, gate_mode,
                         row_gate, slot_row, extra_row, T, d, E, k, dtype, router_grad, dx, dw_gate,
-                        dS, dlogits, TokenWs{w.dl, w.dx_acc, w.dl_hi, w.dl_lo, w.dwg_part}, s);
+                        row_token, offsets, dS, dlogits, TokenWs{w.dl, w.dx_acc, w.dl_hi, w.dl_lo, w.dwg_part}, s);
 }
 
 int moe_layer_bwd(const void* dout, const void* x, const void* w_gate, const void* w1,
@@ -770,7 +772,7 @@ int moe_token_bwd(const void* dX_rows, const float* dS, const void* x, const voi
   if (!c.ok) return fail(MOE_ERR_WORKSPACE, "workspace too small");
   return token_bwd_impl(dX_rows, dS, 1, x, w_gate, idx, gate, gate_grad, logits, gate_mode,
                         row_gate, slot_row, extra_row, T, d, E, k, dtype, router_grad, dx, dw_gate,
-                        nullptr, dlogits, w.w, (cudaStream_t)stream);
+                        nullptr, nullptr, nullptr, dlogits, w.w, (cudaStream_t)stream);
 }
 
 int moe_ep_dispatch_counts(const int32_t* offsets, int E, int32_t* seg_rows, void* stream) {

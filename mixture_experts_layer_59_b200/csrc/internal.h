@@ -54,13 +54,14 @@ int launch_dx_fused(const void* dxp, const int32_t* slot_row, const int32_t* ext
 int launch_token_reduce(const void* src, const float* row_gate, const int32_t* slot_row,
                         const int32_t* extra_row, int T, int width, int E, int k, int dtype,
                         bool weighted, bool out_f32, void* out, cudaStream_t s);
-// dlogits and (optionally) the final dS rows from dS partials [cap, nparts].
+// dlogits and (optionally) the final dS rows [cap] from dS partials [cap, nparts]
+// (0 for the rows without a token; row_token, offsets: read for dS_out only).
 // Optionally also writes dlogits split as bf16 hi + bf16 lo (tensor-core router GEMMs).
 int launch_router_bwd(const float* ds_part, int nparts, const int32_t* idx, const float* gate,
                       const float* row_gate, const int32_t* slot_row, const int32_t* extra_row,
                       const float* gate_grad, const float* logits, int gate_mode, int T, int E,
-                      int k, float* dlogits, float* dS_out, void* dl_hi, void* dl_lo,
-                      cudaStream_t s);
+                      int k, float* dlogits, const int32_t* row_token, const int32_t* offsets,
+                      int cap, float* dS_out, void* dl_hi, void* dl_lo, cudaStream_t s);
 // Load-balance loss lambda*CV^2, routing statistics and dL/dgate.
 size_t balance_ws_bytes(int T, int E);
 int launch_balance_loss(const int32_t* idx, const float* gate, int T, int E, int k, float lam,

@@ -681,16 +681,25 @@ int launch_balance_loss(const int32_t* idx, const float* gate, int T, int E, int
 // One warp per token.  dS of a row = sum of its partials (fixed order).
 //   v_r = row_gate[r] * dS[r] for every row r of token t (expert e_r)
 //   dl[t, e_r] += v_r;  dl[t, idx[t,j]] -= gate[t,j] * sum_r v_r
+// dS_out [cap]: also 0 for the rows without a token (row_token < 0 below
+// offsets[E], and all at or past it).
 __global__ void k_router_bwd(const float* __restrict__ ds_part, int nparts,
                              const int32_t* __restrict__ idx, const float* __restrict__ gate,
                              const float* __restrict__ row_gate, const int32_t* __restrict__ slot_row,
                              const int32_t* __restrict__ extra_row, const float* __restrict__ gate_grad,
                              const float* __restrict__ logits, int gate_mode,
                              int T, int E, int k, float* __restrict__ dlogits,
+                             const int32_t* __restrict__ row_token,
+                             const int32_t* __restrict__ offsets, int cap,
                              float* __restrict__ dS_out, __nv_bfloat16* __restrict__ dl_hi,
                              __nv_bfloat16* __restrict__ dl_lo) {
   __shared__ float s_dl[8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if (dS_out != nullptr) {
+    const int R = offsets[E];
+    for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < cap; r += gridDim.x * blockDim.x)
+      if (r >= R || row_token[r] < 0) dS_out[r] = 0.f;
+  }
   float* dl = s_dl[w];
   for (int t = blockIdx.x * 8 + w; t < T; t += gridDim.x * 8) {
     for (int e = lane; e < E; e += 32) dl[e] = 0.f;
@@ -784,16 +793,21 @@ __global__ void k_router_bwd(const float* __restrict__ ds_part, int nparts,
 int launch_router_bwd(const float* ds_part, int nparts, const int32_t* idx, const float* gate,
                       const float* row_gate, const int32_t* slot_row, const int32_t* extra_row,
                       const float* gate_grad, const float* logits, int gate_mode, int T, int E,
-                      int k, float* dlogits, float* dS_out, void* dl_hi, void* dl_lo,
-                      cudaStream_t s) {
-  if (T == 0) return MOE_OK;
+                      int k, float* dlogits, const int32_t* row_token, const int32_t* offsets,
+                      int cap, float* dS_out, void* dl_hi, void* dl_lo, cudaStream_t s) {
+  if (T == 0) {
+    if (dS_out != nullptr)
+      if (cudaError_t e = cudaMemsetAsync(dS_out, 0, (size_t)cap * sizeof(float), s))
+        return cuda_fail(e, "memset dS");
+    return MOE_OK;
+  }
   int blocks = (T + 7) / 8;
   if (blocks > device_sm_count() * 16) blocks = device_sm_count() * 16;
   {
     ProfScope _ps("router_bwd", s);
     k_router_bwd<<<blocks, 256, 0, s>>>(ds_part, nparts, idx, gate, row_gate, slot_row, extra_row,
-                                        gate_grad, logits, gate_mode, T, E, k, dlogits, dS_out,
-                                        (__nv_bfloat16*)dl_hi,
+                                        gate_grad, logits, gate_mode, T, E, k, dlogits, row_token,
+                                        offsets, cap, dS_out, (__nv_bfloat16*)dl_hi,
                                         (__nv_bfloat16*)dl_lo);
   }
   MOE_CHECK_LAUNCH("router_bwd");
