@@ -564,9 +564,10 @@ int moe_check_status(void* stream);
  * of this process) of a tensor-core GEMM or of the layer norm's backward pass
  * over many rows runs with its producer issuing no copies and every bounded
  * wait limited to wait_ns nanoseconds, so that the wait for a full stage
- * expires with nothing in flight; the hook then resets itself.  That launch's outputs are undefined and
- * moe_check_status() afterwards returns MOE_ERR_DEVICE_TIMEOUT.  wait_ns <= 0
- * cancels a pending request.  Returns MOE_OK.
+ * expires with nothing in flight; the hook then resets itself.  That launch's
+ * outputs are undefined and moe_check_status() afterwards returns
+ * MOE_ERR_DEVICE_TIMEOUT.  wait_ns <= 0 cancels a pending request.  Returns
+ * MOE_OK.
  * moe_debug_expire_later_wait -- the same after `skip` such launches have
  * passed as usual (a later product of one call).
  */

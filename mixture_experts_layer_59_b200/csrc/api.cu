@@ -594,7 +594,8 @@ static int layer_bwd_impl(const void* dout, const void* x, const void* w_gate, c
   }
   return token_bwd_impl(w.dxp, w.ds, w.nparts, x, w_gate, idx, gate, gate_grad, logits, gate_mode,
                         row_gate, slot_row, extra_row, T, d, E, k, dtype, router_grad, dx, dw_gate,
-                        row_token, offsets, dS, dlogits, TokenWs{w.dl, w.dx_acc, w.dl_hi, w.dl_lo, w.dwg_part}, s);
+                        row_token, offsets, dS, dlogits,
+                        TokenWs{w.dl, w.dx_acc, w.dl_hi, w.dl_lo, w.dwg_part}, s);
 }
 
 int moe_layer_bwd(const void* dout, const void* x, const void* w_gate, const void* w1,
